@@ -54,7 +54,7 @@ typedef struct {
     int64_t shared_blocks;  /* refcount > 1 */
     int64_t num_seqs;       /* live sequences */
     int64_t logical_tokens; /* sum of the sequences' token counts */
-    int64_t logical_blocks; /* sum of the sequences' table lengths */
+    int64_t logical_blocks; /* sum of the sequences' table lengths (trimmed entries excluded) */
     int64_t filled_slots;   /* slots of used blocks that hold a token */
     int64_t cow_copies;     /* copy pairs emitted since creation */
     int64_t cached_blocks;  /* full blocks findable by content (prefix caching) */
@@ -103,11 +103,26 @@ int pa_alloc_append_slots(pa_alloc *a, const int64_t *seq_ids, int32_t n, int64_
  * of the free list at once. */
 int pa_alloc_free_seq(pa_alloc *a, int64_t seq_id);
 
+/* Drop the blocks of seq_id that a sliding window has left behind: those all
+ * of whose tokens are out of sight (neither in the window nor among the first
+ * num_sinks) for every query at position next_position or later, as
+ * pa_decode_window and pa_prefill_window define it.  next_position is the
+ * position of the sequence's next query (L - 1 before the decode of its L-th
+ * token, the first row of the next chunk during prefill).  Each such block
+ * loses one reference (0: back of the free list; a prefix-cached block stays
+ * findable) and its table entry becomes -1.  The last, partly filled block is
+ * never among them, so appending is unaffected; a later fork shares the
+ * remaining blocks only.  Returns the number of entries dropped, or
+ * PA_ERR_INVALID_ARG (unknown sequence, window < 1, num_sinks < 0,
+ * next_position outside [0, token count]). */
+int32_t pa_alloc_trim_window(pa_alloc *a, int64_t seq_id, int32_t next_position, int32_t window,
+                             int32_t num_sinks);
+
 /* Token count of seq_id, or PA_ERR_INVALID_ARG if unknown. */
 int32_t pa_alloc_num_tokens(const pa_alloc *a, int64_t seq_id);
 
-/* Copy seq_id's block table into out (at most cap entries); returns its
- * length, or PA_ERR_INVALID_ARG. */
+/* Copy seq_id's block table into out (at most cap entries; -1 for trimmed
+ * ones); returns its length, or PA_ERR_INVALID_ARG. */
 int32_t pa_alloc_block_table(const pa_alloc *a, int64_t seq_id, int32_t *out, int32_t cap);
 
 /* Padded table matrix for a batch: row i of tables ([n][max_blocks], host)

@@ -291,6 +291,135 @@ int pa_decode_static_workspace(void *out, const void *q, const void *key_cache,
                                int32_t dtype, void *stream);
 
 /*
+ * pa_decode_window, pa_decode_append_window - pa_decode and pa_decode_append
+ * with a sliding window and attention sinks.
+ *
+ * The pages have no counterpart: a windowed model attends to its last tokens
+ * and to a few first ones, and the cache may drop what lies between
+ * (pa_alloc_trim_window).
+ *
+ * The query sits at position p = L - 1 (L = context_lens[s]) and sees token
+ * j < L when p - j < window or j < num_sinks; the sums of pa_decode run over
+ * the tokens seen.  Only the table entries of blocks that hold such a token
+ * are read; the others may hold anything (-1 after a trim).  Tokens not seen
+ * may hold anything, NaN included, also inside a block that is read.
+ * window >= 1 (PA_ERR_INVALID_ARG otherwise; a window of 2^30 or more means
+ * all), num_sinks >= 0, max_blocks_per_seq <= 2^26.  Everything else is as in
+ * pa_decode / pa_decode_append, except that q and out must start on a 16-byte
+ * boundary and that the workspace's size comes from
+ * pa_decode_window_workspace_size for the same arguments (0: may be NULL).
+ * A row's partitions are joined in a fixed order: equal calls give equal bits.
+ */
+int pa_decode_window(void *out, const void *q, const void *key_cache, const void *value_cache,
+                     const int32_t *block_tables, const int32_t *context_lens, int32_t window,
+                     int32_t num_sinks, int32_t num_kv_heads, float scale, int32_t num_seqs,
+                     int32_t num_q_heads, int32_t head_dim, int32_t block_size,
+                     int32_t max_blocks_per_seq, int64_t num_blocks, int32_t dtype,
+                     void *workspace, size_t workspace_bytes, void *stream);
+int pa_decode_append_window(void *out, const void *q, const void *k_new, const void *v_new,
+                            void *key_cache, void *value_cache, const int32_t *block_tables,
+                            const int32_t *context_lens, int32_t window, int32_t num_sinks,
+                            int32_t num_kv_heads, float scale, int32_t num_seqs,
+                            int32_t num_q_heads, int32_t head_dim, int32_t block_size,
+                            int32_t max_blocks_per_seq, int64_t num_blocks, int32_t dtype,
+                            void *workspace, size_t workspace_bytes, void *stream);
+size_t pa_decode_window_workspace_size(int32_t num_seqs, int32_t num_q_heads, int32_t num_kv_heads,
+                                       int32_t head_dim, int32_t block_size,
+                                       int32_t max_blocks_per_seq, int32_t window,
+                                       int32_t num_sinks);
+
+/*
+ * pa_prefill_window - pa_prefill with a sliding window and attention sinks.
+ *
+ * Query row i of sequence s sits at position p = L - n_s + i, as in
+ * pa_prefill, and sees token j when j <= p and (p - j < window or
+ * j < num_sinks).  Table entries of blocks that no row of the chunk sees are
+ * not read.  Tokens that no row of the chunk sees may hold anything; a token
+ * that some row sees must be finite, since rows that do not see it still
+ * multiply its value by a zero weight.
+ *
+ * Chunks of up to 16 query rows per kv head (max_query_len times the group)
+ * run on the decode kernel, longer ones on the tcgen05 kernel
+ * (pa_prefill_select does not matter here).  Either splits a row's keys when
+ * there is too little work for the GPU; the parts go to `workspace`
+ * (pa_prefill_window_workspace_size bytes for the same arguments, 256-byte
+ * aligned; may be NULL when that is 0) and are joined in a fixed order.  Calls
+ * that share a workspace must not overlap.
+ *
+ * window and num_sinks as in pa_decode_window.  q and out start on 16-byte
+ * boundaries.  PA_ERR_UNSUPPORTED for scale <= 0 or not finite, and for more
+ * than 128 query heads per kv head.  A chunk longer than max_query_len sets
+ * PA_DEVERR_CONTEXT_LEN and its rows are left as they were.  Rows of q / out
+ * past query_start[num_seqs] are not touched.
+ */
+int pa_prefill_window(void *out, const void *q, const void *key_cache, const void *value_cache,
+                      const int32_t *block_tables, const int32_t *context_lens,
+                      const int32_t *query_start, int32_t max_query_len, int32_t window,
+                      int32_t num_sinks, int32_t num_kv_heads, float scale, int32_t num_seqs,
+                      int32_t num_q_heads, int32_t num_q_tokens, int32_t head_dim,
+                      int32_t block_size, int32_t max_blocks_per_seq, int64_t num_blocks,
+                      int32_t dtype, void *workspace, size_t workspace_bytes, void *stream);
+size_t pa_prefill_window_workspace_size(int32_t num_seqs, int32_t num_q_tokens,
+                                        int32_t max_query_len, int32_t num_q_heads,
+                                        int32_t num_kv_heads, int32_t head_dim, int32_t block_size,
+                                        int32_t max_blocks_per_seq, int32_t window,
+                                        int32_t num_sinks);
+
+/*
+ * Rotary positions: which angle each pair of a head's elements turns by.  The
+ * caller keeps one per model (pa_rope_init) and passes it to every call.
+ *
+ * Pair i (i < num_pairs) of a head of head_dim elements is elements
+ * (i, i + num_pairs), or (2i, 2i + 1) when interleaved; elements from
+ * 2 * num_pairs on are not turned.  It turns by
+ *   angle = positions[pair_axes[i]][t] * inv_freq[i]
+ * so that a token may have several positions (time, height, width).
+ */
+#define PA_ROPE_MAX_PAIRS 64
+#define PA_ROPE_MAX_AXES 8
+typedef struct {
+    uint64_t turns[PA_ROPE_MAX_PAIRS]; /* inv_freq / (2 pi) modulo 1, times 2^64 */
+    uint8_t axis[PA_ROPE_MAX_PAIRS];
+    int32_t num_pairs, num_axes, interleaved;
+} pa_rope;
+
+/* Fill *rope.  inv_freq: host, [num_pairs], finite; pair_axes: host,
+ * [num_pairs], values in [0, num_axes), or NULL for axis 0 everywhere.
+ * num_pairs is a multiple of 8 up to 64, num_axes at most 8
+ * (PA_ERR_UNSUPPORTED otherwise).  On an error *rope is left as it was. */
+int pa_rope_init(pa_rope *rope, const float *inv_freq, const int32_t *pair_axes, int32_t num_pairs,
+                 int32_t num_axes, int32_t interleaved);
+
+/*
+ * pa_rope_and_cache - turn q and k by their positions, and write k and v into
+ * their cache slots: what precedes pa_decode_window in a step, in one launch.
+ *
+ * For each token t: q_out[t][h] = turned q[t][h] for every query head, and if
+ * slot = slot_mapping[t] >= 0 the turned k[t][g] and v[t][g] (as it is) go to
+ * that slot for every kv head, as in pa_reshape_and_cache (negative: padding;
+ * beyond the pool: skipped, PA_DEVERR_SLOT; two tokens with one slot race).
+ * The angle is exact modulo a turn for every int32 position; cos and sin are
+ * taken in f32, the products summed in f32 and rounded once to dtype.
+ *
+ *   q, k, v       device, dtype; token t's heads start at t * stride elements
+ *                 (strides >= 0 and multiples of 8, so the three may be slices
+ *                 of one projection's output), each head's head_dim elements
+ *                 and the heads contiguous, 16-byte aligned
+ *   q_out         device, [num_tokens][num_q_heads][head_dim], contiguous; may
+ *                 be q itself if q is contiguous too
+ *   positions     device, int32 [num_axes][num_tokens], any values
+ *   slot_mapping  device, int64 [num_tokens]
+ *   rope          host
+ * num_q_heads may be 0 (k and v only; q and q_out unused).
+ */
+int pa_rope_and_cache(void *q_out, const void *q, const void *k, const void *v, void *key_cache,
+                      void *value_cache, const int64_t *slot_mapping, const int32_t *positions,
+                      const pa_rope *rope, int64_t q_stride, int64_t k_stride, int64_t v_stride,
+                      int32_t num_tokens, int32_t num_q_heads, int32_t num_kv_heads,
+                      int32_t head_dim, int32_t block_size, int64_t num_blocks, int32_t dtype,
+                      void *stream);
+
+/*
  * pa_copy_blocks - copy-on-write block copies.
  *
  * Source: "Inside vLLM ...", section "Copy-on-Write Makes Beam Search Cheap";

@@ -63,6 +63,14 @@ class SimStats(ctypes.Structure):
                 ("mean_usage", _f64), ("max_usage", _f64), ("mean_running", _f64)]
 
 
+ROPE_MAX_PAIRS = 64  # PA_ROPE_MAX_PAIRS
+
+
+class RopeStruct(ctypes.Structure):
+    _fields_ = [("turns", ctypes.c_uint64 * ROPE_MAX_PAIRS), ("axis", ctypes.c_uint8 * ROPE_MAX_PAIRS),
+                ("num_pairs", _i32), ("num_axes", _i32), ("interleaved", _i32)]
+
+
 class AllocStats(ctypes.Structure):
     _fields_ = [("num_blocks", _i64), ("free_blocks", _i64), ("used_blocks", _i64),
                 ("shared_blocks", _i64), ("num_seqs", _i64), ("logical_tokens", _i64),
@@ -84,6 +92,23 @@ pa_decode_static_workspace = _sig("pa_decode_static_workspace", ctypes.c_int, _P
 pa_prefill = _sig("pa_prefill", ctypes.c_int, _P, _P, _P, _P, _P, _P, _P, _i32, _i32, _f32, _i32,
                   _i32, _i32, _i32, _i32, _i32, _i64, _i32, _P)
 pa_prefill_select = _sig("pa_prefill_select", ctypes.c_int, _i32)
+pa_decode_window = _sig("pa_decode_window", ctypes.c_int, _P, _P, _P, _P, _P, _P, _i32, _i32, _i32,
+                        _f32, _i32, _i32, _i32, _i32, _i32, _i64, _i32, _P, _sz, _P)
+pa_decode_append_window = _sig("pa_decode_append_window", ctypes.c_int, _P, _P, _P, _P, _P, _P, _P,
+                               _P, _i32, _i32, _i32, _f32, _i32, _i32, _i32, _i32, _i32, _i64, _i32,
+                               _P, _sz, _P)
+pa_decode_window_workspace_size = _sig("pa_decode_window_workspace_size", _sz, _i32, _i32, _i32,
+                                       _i32, _i32, _i32, _i32, _i32)
+pa_prefill_window = _sig("pa_prefill_window", ctypes.c_int, _P, _P, _P, _P, _P, _P, _P, _i32, _i32,
+                         _i32, _i32, _f32, _i32, _i32, _i32, _i32, _i32, _i32, _i64, _i32, _P, _sz,
+                         _P)
+pa_prefill_window_workspace_size = _sig("pa_prefill_window_workspace_size", _sz, _i32, _i32, _i32,
+                                        _i32, _i32, _i32, _i32, _i32, _i32, _i32)
+pa_rope_init = _sig("pa_rope_init", ctypes.c_int, ctypes.POINTER(RopeStruct), _P, _P, _i32, _i32,
+                    _i32)
+pa_rope_and_cache = _sig("pa_rope_and_cache", ctypes.c_int, _P, _P, _P, _P, _P, _P, _P, _P,
+                         ctypes.POINTER(RopeStruct), _i64, _i64, _i64, _i32, _i32, _i32, _i32, _i32,
+                         _i64, _i32, _P)
 pa_copy_blocks = _sig("pa_copy_blocks", ctypes.c_int, _P, _P, _P, _i32, _i32, _i32, _i32, _i64,
                       _i32, _P)
 pa_swap_blocks = _sig("pa_swap_blocks", ctypes.c_int, _P, _P, _i64, _P, _P, _i64, _P, _i32, _i32,
@@ -101,6 +126,7 @@ pa_alloc_append_slot = _sig("pa_alloc_append_slot", ctypes.c_int, _P, _i64,
 pa_alloc_append_slots = _sig("pa_alloc_append_slots", ctypes.c_int, _P, _P, _i32, _P, _P,
                              ctypes.POINTER(_i32))
 pa_alloc_free_seq = _sig("pa_alloc_free_seq", ctypes.c_int, _P, _i64)
+pa_alloc_trim_window = _sig("pa_alloc_trim_window", _i32, _P, _i64, _i32, _i32, _i32)
 pa_alloc_num_tokens = _sig("pa_alloc_num_tokens", _i32, _P, _i64)
 pa_alloc_block_table = _sig("pa_alloc_block_table", _i32, _P, _i64, _P, _i32)
 pa_alloc_build_tables = _sig("pa_alloc_build_tables", ctypes.c_int, _P, _P, _i32, _P, _i32, _P)
@@ -267,6 +293,206 @@ def prefill(out, q, key_cache, value_cache, block_tables, context_lens, query_st
                       _stream(stream)), "pa_prefill")
 
 
+# ---------------------------------------------------------------- sliding window, rotary positions
+def _one_device(tensors):
+    """Every tensor on the current CUDA device (the launch goes there)."""
+    dev = _torch().cuda.current_device()
+    for t in tensors:
+        if t.get_device() != dev:
+            raise ValueError(f"every tensor must be on the current CUDA device {dev}, got {t.device}")
+
+
+def _i32_arg(x, name):
+    x = int(x)
+    if not -2 ** 31 <= x < 2 ** 31:
+        raise ValueError(f"{name} must fit 32 bits, got {x}")
+    return x
+
+
+def _workspace(workspace):
+    if workspace is None:
+        return None, 0
+    _one_device((workspace,))
+    return _dev(workspace, "workspace"), workspace.numel() * workspace.element_size()
+
+
+def _window_shapes(out, q, key_cache, value_cache, block_tables, context_lens, num_kv_heads):
+    """Shared checks of the windowed calls -> (num_blocks, d, block size, Hq)."""
+    nb, hkv, bs, d = _cache_shape(key_cache, value_cache)
+    if hkv != num_kv_heads:
+        raise ValueError("num_kv_heads does not match the cache")
+    rows, hq, dq = q.shape
+    if dq != d or out.shape != q.shape or out.dtype != q.dtype or q.dtype != key_cache.dtype:
+        raise ValueError("q / out must be [rows, Hq, d] of the cache dtype")
+    S = context_lens.shape[0]
+    if block_tables.dim() != 2 or block_tables.shape[0] != S or context_lens.dim() != 1:
+        raise ValueError("block_tables must be [S, max_blocks], context_lens [S]")
+    return nb, d, bs, hq
+
+
+def decode_window_workspace_size(num_seqs: int, num_q_heads: int, num_kv_heads: int, head_dim: int,
+                                 max_blocks_per_seq: int, window: int, num_sinks: int = 0,
+                                 block_size: int = BLOCK_SIZE) -> int:
+    return int(pa_decode_window_workspace_size(num_seqs, num_q_heads, num_kv_heads, head_dim,
+                                               block_size, max_blocks_per_seq,
+                                               _i32_arg(window, "window"),
+                                               _i32_arg(num_sinks, "num_sinks")))
+
+
+def decode_window(out, q, key_cache, value_cache, block_tables, context_lens, num_kv_heads: int,
+                  scale: float, window: int, num_sinks: int = 0, workspace=None, stream=None):
+    """decode over a sliding window and the first tokens: the query at position
+    p = context_lens[s] - 1 sees token j when p - j < window or j < num_sinks.
+    Table entries of blocks without such a token are not read."""
+    torch = _torch()
+    nb, d, bs, hq = _window_shapes(out, q, key_cache, value_cache, block_tables, context_lens,
+                                   num_kv_heads)
+    S = q.shape[0]
+    if context_lens.shape[0] != S:
+        raise ValueError("context_lens must be [S]")
+    _one_device((out, q, key_cache, value_cache, block_tables, context_lens))
+    ws_ptr, ws_bytes = _workspace(workspace)
+    _check(pa_decode_window(_dev(out, "out"), _dev(q, "q"), _dev(key_cache, "key_cache"),
+                            _dev(value_cache, "value_cache"),
+                            _dev(block_tables, "block_tables", torch.int32),
+                            _dev(context_lens, "context_lens", torch.int32),
+                            _i32_arg(window, "window"), _i32_arg(num_sinks, "num_sinks"),
+                            num_kv_heads, float(scale), S, hq, d, bs, block_tables.shape[1], nb,
+                            dtype_code(q), ws_ptr, ws_bytes, _stream(stream)), "pa_decode_window")
+
+
+def decode_append_window(out, q, k_new, v_new, key_cache, value_cache, block_tables, context_lens,
+                         num_kv_heads: int, scale: float, window: int, num_sinks: int = 0,
+                         workspace=None, stream=None):
+    """decode_append over a sliding window and the first tokens (decode_window)."""
+    torch = _torch()
+    nb, d, bs, hq = _window_shapes(out, q, key_cache, value_cache, block_tables, context_lens,
+                                   num_kv_heads)
+    S = q.shape[0]
+    if context_lens.shape[0] != S:
+        raise ValueError("context_lens must be [S]")
+    for name, t in (("k_new", k_new), ("v_new", v_new)):
+        if tuple(t.shape) != (S, num_kv_heads, d) or t.dtype != key_cache.dtype:
+            raise ValueError(f"{name} must be [S, Hkv, d] of the cache dtype")
+    _one_device((out, q, k_new, v_new, key_cache, value_cache, block_tables, context_lens))
+    ws_ptr, ws_bytes = _workspace(workspace)
+    _check(pa_decode_append_window(_dev(out, "out"), _dev(q, "q"), _dev(k_new, "k_new"),
+                                   _dev(v_new, "v_new"), _dev(key_cache, "key_cache"),
+                                   _dev(value_cache, "value_cache"),
+                                   _dev(block_tables, "block_tables", torch.int32),
+                                   _dev(context_lens, "context_lens", torch.int32),
+                                   _i32_arg(window, "window"), _i32_arg(num_sinks, "num_sinks"),
+                                   num_kv_heads, float(scale), S, hq, d, bs,
+                                   block_tables.shape[1], nb, dtype_code(q), ws_ptr, ws_bytes,
+                                   _stream(stream)), "pa_decode_append_window")
+
+
+def prefill_window_workspace_size(num_seqs: int, num_q_tokens: int, max_query_len: int,
+                                  num_q_heads: int, num_kv_heads: int, head_dim: int,
+                                  max_blocks_per_seq: int, window: int, num_sinks: int = 0,
+                                  block_size: int = BLOCK_SIZE) -> int:
+    return int(pa_prefill_window_workspace_size(num_seqs, num_q_tokens, max_query_len, num_q_heads,
+                                                num_kv_heads, head_dim, block_size,
+                                                max_blocks_per_seq, _i32_arg(window, "window"),
+                                                _i32_arg(num_sinks, "num_sinks")))
+
+
+def prefill_window(out, q, key_cache, value_cache, block_tables, context_lens, query_start,
+                   max_query_len: int, num_kv_heads: int, scale: float, window: int,
+                   num_sinks: int = 0, workspace=None, stream=None):
+    """Chunked prefill over a sliding window and the first tokens: the row at
+    position p sees token j when j <= p and (p - j < window or j < num_sinks)."""
+    torch = _torch()
+    nb, d, bs, hq = _window_shapes(out, q, key_cache, value_cache, block_tables, context_lens,
+                                   num_kv_heads)
+    S = context_lens.shape[0]
+    if query_start.shape != (S + 1,):
+        raise ValueError("query_start must be [S + 1]")
+    _one_device((out, q, key_cache, value_cache, block_tables, context_lens, query_start))
+    ws_ptr, ws_bytes = _workspace(workspace)
+    _check(pa_prefill_window(_dev(out, "out"), _dev(q, "q"), _dev(key_cache, "key_cache"),
+                             _dev(value_cache, "value_cache"),
+                             _dev(block_tables, "block_tables", torch.int32),
+                             _dev(context_lens, "context_lens", torch.int32),
+                             _dev(query_start, "query_start", torch.int32),
+                             _i32_arg(max_query_len, "max_query_len"), _i32_arg(window, "window"),
+                             _i32_arg(num_sinks, "num_sinks"), num_kv_heads, float(scale), S, hq,
+                             q.shape[0], d, bs, block_tables.shape[1], nb, dtype_code(q), ws_ptr,
+                             ws_bytes, _stream(stream)), "pa_prefill_window")
+
+
+class Rope:
+    """Rotary positions of a model: pair i of a head turns by
+    positions[pair_axes[i]] * inv_freq[i].
+
+    inv_freq: [pairs] (used as float32); pair_axes: [pairs] axis numbers, or
+    None for a single axis; interleaved: pairs are (2i, 2i + 1) instead of
+    (i, i + pairs); num_axes: rows of the positions tensor (default: the
+    largest axis used, plus one)."""
+
+    def __init__(self, inv_freq, pair_axes=None, interleaved: bool = False, num_axes: int | None = None):
+        freq = np.ascontiguousarray(inv_freq, dtype=np.float32)
+        if freq.ndim != 1 or not freq.size:
+            raise ValueError("inv_freq must be [pairs]")
+        axes = None
+        if pair_axes is not None:
+            axes = np.ascontiguousarray(pair_axes, dtype=np.int32)
+            if axes.shape != freq.shape:
+                raise ValueError("pair_axes must have one axis per pair")
+        if num_axes is None:
+            num_axes = 1 if axes is None else int(axes.max()) + 1
+        self._struct = RopeStruct()
+        _check(pa_rope_init(ctypes.byref(self._struct), freq.ctypes.data,
+                            None if axes is None else axes.ctypes.data, int(freq.size),
+                            int(num_axes), int(bool(interleaved))), "pa_rope_init")
+        self._ref = ctypes.byref(self._struct)
+        self.num_pairs = int(freq.size)
+        self.num_axes = int(num_axes)
+        self.interleaved = bool(interleaved)
+
+
+def _rows(t, name, heads, d, dtype):
+    """Pointer and token stride of [T][heads][d] whose heads lie contiguously."""
+    if t.dim() != 3 or t.shape[1] != heads or t.shape[2] != d or t.dtype != dtype:
+        raise ValueError(f"{name} must be [T, {heads}, {d}] {dtype}, got {tuple(t.shape)} {t.dtype}")
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    st, sh, sd = t.stride()
+    if t.numel() and ((d > 1 and sd != 1) or (heads > 1 and sh != d)):
+        raise ValueError(f"{name}: the heads of a token must be contiguous")
+    return ctypes.c_void_p(t.data_ptr()), st if t.shape[0] > 1 else 0
+
+
+def rope_and_cache(q_out, q, k, v, key_cache, value_cache, slot_mapping, positions, rope: Rope,
+                   stream=None):
+    """Turn q and k by their positions and write k, v into their slots.
+
+    q [T][Hq][d], k and v [T][Hkv][d] may be slices of one projection's output
+    (any token stride that is a multiple of 8); q_out [T][Hq][d] contiguous
+    (q itself if contiguous); positions int32 [rope.num_axes][T];
+    slot_mapping int64 [T], negative for padding."""
+    torch = _torch()
+    nb, hkv, bs, d = _cache_shape(key_cache, value_cache)
+    T = slot_mapping.shape[0]
+    hq = q.shape[1]
+    if q_out.shape != q.shape or q_out.dtype != q.dtype:
+        raise ValueError("q_out must be like q")
+    if q.shape[0] != T or k.shape[0] != T or v.shape[0] != T:
+        raise ValueError(f"q, k and v must have {T} tokens")
+    if tuple(positions.shape) != (rope.num_axes, T):
+        raise ValueError(f"positions must be [{rope.num_axes}, {T}]")
+    _one_device((q_out, q, k, v, key_cache, value_cache, slot_mapping, positions))
+    qp, qs = _rows(q, "q", hq, d, key_cache.dtype)
+    kp, ks = _rows(k, "k", hkv, d, key_cache.dtype)
+    vp, vs = _rows(v, "v", hkv, d, key_cache.dtype)
+    _check(pa_rope_and_cache(_dev(q_out, "q_out"), qp, kp, vp, _dev(key_cache, "key_cache"),
+                             _dev(value_cache, "value_cache"),
+                             _dev(slot_mapping, "slot_mapping", torch.int64, 1),
+                             _dev(positions, "positions", torch.int32, 2), rope._ref, qs, ks, vs, T,
+                             hq, hkv, d, bs, nb, dtype_code(key_cache), _stream(stream)),
+           "pa_rope_and_cache")
+
+
 PREFILL_KERNELS = {"auto": 0, "mma_sync": 1, "tcgen05": 2}
 
 
@@ -406,6 +632,13 @@ class BlockAllocator:
 
     def free_seq(self, seq_id: int):
         _check(pa_alloc_free_seq(self._h, seq_id), "pa_alloc_free_seq")
+
+    def trim_window(self, seq_id: int, next_position: int, window: int, num_sinks: int = 0) -> int:
+        """Drop the blocks no query at next_position or later can see; returns
+        how many.  Their table entries become -1."""
+        n = pa_alloc_trim_window(self._h, seq_id, next_position, window, num_sinks)
+        _check(min(n, 0), "pa_alloc_trim_window")
+        return n
 
     def num_tokens(self, seq_id: int) -> int:
         n = pa_alloc_num_tokens(self._h, seq_id)

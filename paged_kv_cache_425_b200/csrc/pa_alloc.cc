@@ -24,7 +24,7 @@
 namespace {
 
 struct Sequence {
-    std::vector<int32_t> blocks;  // logical block i -> physical block
+    std::vector<int32_t> blocks;  // logical block i -> physical block, -1 once trimmed
     int32_t num_tokens = 0;
 };
 
@@ -135,7 +135,8 @@ int pa_alloc_fork(pa_alloc *a, int64_t parent_id, int64_t child_id) {
     auto it = a->seqs.find(parent_id);
     if (it == a->seqs.end()) return PA_ERR_INVALID_ARG;
     Sequence child = it->second;
-    for (int32_t b : child.blocks) ++a->refcount[b];
+    for (int32_t b : child.blocks)
+        if (b >= 0) ++a->refcount[b];
     a->seqs.emplace(child_id, std::move(child));
     return PA_OK;
 }
@@ -194,9 +195,31 @@ int pa_alloc_free_seq(pa_alloc *a, int64_t seq_id) {
     if (!a) return PA_ERR_INVALID_ARG;
     auto it = a->seqs.find(seq_id);
     if (it == a->seqs.end()) return PA_ERR_INVALID_ARG;
-    for (int32_t b : it->second.blocks) a->release(b);
+    for (int32_t b : it->second.blocks)
+        if (b >= 0) a->release(b);
     a->seqs.erase(it);
     return PA_OK;
+}
+
+int32_t pa_alloc_trim_window(pa_alloc *a, int64_t seq_id, int32_t next_position, int32_t window,
+                             int32_t num_sinks) {
+    if (!a || window < 1 || num_sinks < 0 || next_position < 0) return PA_ERR_INVALID_ARG;
+    auto it = a->seqs.find(seq_id);
+    if (it == a->seqs.end() || next_position > it->second.num_tokens) return PA_ERR_INVALID_ARG;
+    // a query at next_position sees tokens above next_position - window; later
+    // ones see no earlier token
+    const int64_t bs = a->block_size;
+    const int64_t first = ((int64_t)num_sinks + bs - 1) / bs;         // first block without a sink
+    const int64_t end = ((int64_t)next_position - window + 1) / bs;   // blocks wholly out of the window
+    int32_t dropped = 0;
+    for (int64_t i = first; i < end; ++i) {
+        int32_t &b = it->second.blocks[i];
+        if (b < 0) continue;
+        a->release(b);
+        b = -1;
+        ++dropped;
+    }
+    return dropped;
 }
 
 int32_t pa_alloc_num_tokens(const pa_alloc *a, int64_t seq_id) {
@@ -248,8 +271,9 @@ int pa_alloc_get_stats(const pa_alloc *a, pa_alloc_stats *out) {
     for (const auto &kv : a->seqs) {
         const Sequence &s = kv.second;
         st.logical_tokens += s.num_tokens;
-        st.logical_blocks += (int64_t)s.blocks.size();
         for (size_t i = 0; i < s.blocks.size(); ++i) {
+            if (s.blocks[i] < 0) continue;
+            ++st.logical_blocks;
             int64_t in_block = (int64_t)s.num_tokens - (int64_t)i * a->block_size;
             int32_t n = (int32_t)(in_block > a->block_size ? a->block_size : in_block);
             if (n > filled[s.blocks[i]]) filled[s.blocks[i]] = n;

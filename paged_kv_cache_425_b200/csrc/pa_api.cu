@@ -6,14 +6,18 @@
 #include <cstdint>
 #include <algorithm>
 #include <atomic>
+#include <cmath>
 #include <cstring>
 #include <mutex>
+#include <type_traits>
 #include <utility>
 #include <vector>
 
 #include "pa_api.h"
 #include "pa_kernels.cuh"
 #include "pa_prefill_umma.cuh"
+#include "pa_rope.cuh"
+#include "pa_window.cuh"
 
 namespace pa {
 namespace {
@@ -328,7 +332,7 @@ int launch_prefill_umma(void *out, const void *q, const void *key_cache, const v
                         const int32_t *query_start, int32_t max_query_len, int32_t num_kv_heads,
                         float scale, int32_t num_seqs, int32_t num_q_heads, int32_t num_q_tokens,
                         int32_t head_dim, int32_t max_blocks_per_seq, int64_t num_blocks,
-                        int32_t dtype, cudaStream_t st) {
+                        int32_t dtype, const PrefillWindow *pw, cudaStream_t st) {
     const int group = num_q_heads / num_kv_heads;
     const int tokens_per_tile = kUmmaRows / group;
     const int64_t rows_per_cta = (int64_t)kUmmaQTiles * tokens_per_tile * group;
@@ -353,7 +357,7 @@ int launch_prefill_umma(void *out, const void *q, const void *key_cache, const v
         !encode_cache_map(&tmk, key_cache, num_blocks, num_kv_heads, head_dim, dtype) ||
         !encode_cache_map(&tmv, value_cache, num_blocks, num_kv_heads, head_dim, dtype))
         return PA_ERR_CUDA;
-    const int64_t items = (int64_t)num_seqs * num_kv_heads * tiles;
+    const int64_t items = (int64_t)num_seqs * num_kv_heads * tiles * (pw ? pw->splits : 1);
     if (items >= (int64_t(1) << 31)) return PA_ERR_UNSUPPORTED;
     // persistent: one CTA per SM (tensor memory and shared memory allow no
     // second), each walking its share of the items
@@ -369,13 +373,18 @@ int launch_prefill_umma(void *out, const void *q, const void *key_cache, const v
         if (regs < 0) return PA_ERR_CUDA;
         if ((int64_t)regs * kUmmaThreads < kUmmaRegsNeeded) return PA_ERR_UNSUPPORTED;
         if (!set_smem(kernel, smem)) return PA_ERR_CUDA;
-        return launch_pdl(kernel, grid, dim3(kUmmaThreads), (size_t)smem, st, tmq, tmk, tmv, a);
+        return launch_pdl(kernel, grid, dim3(kUmmaThreads), (size_t)smem, st, tmq, tmk, tmv, a,
+                          pw ? *pw : PrefillWindow{});
     };
-    if (dtype == PA_F16)
-        return head_dim == 128 ? launch(prefill_umma_kernel<__half, 128>)
-                               : launch(prefill_umma_kernel<__half, 64>);
-    return head_dim == 128 ? launch(prefill_umma_kernel<__nv_bfloat16, 128>)
-                           : launch(prefill_umma_kernel<__nv_bfloat16, 64>);
+    auto pick = [&](auto win) -> int {
+        constexpr bool WIN = decltype(win)::value;
+        if (dtype == PA_F16)
+            return head_dim == 128 ? launch(prefill_umma_kernel<__half, 128, WIN>)
+                                   : launch(prefill_umma_kernel<__half, 64, WIN>);
+        return head_dim == 128 ? launch(prefill_umma_kernel<__nv_bfloat16, 128, WIN>)
+                               : launch(prefill_umma_kernel<__nv_bfloat16, 64, WIN>);
+    };
+    return pw ? pick(std::true_type{}) : pick(std::false_type{});
 }
 
 }  // namespace
@@ -575,7 +584,7 @@ int pa_prefill(void *out, const void *q, const void *key_cache, const void *valu
         const int urc = launch_prefill_umma(out, q, key_cache, value_cache, block_tables,
                                             context_lens, query_start, max_query_len, num_kv_heads,
                                             scale, num_seqs, num_q_heads, num_q_tokens, head_dim,
-                                            max_blocks_per_seq, num_blocks, dtype,
+                                            max_blocks_per_seq, num_blocks, dtype, nullptr,
                                             static_cast<cudaStream_t>(stream));
         if (urc != PA_ERR_UNSUPPORTED || which == PA_PREFILL_TCGEN05) return urc;
     }
@@ -737,6 +746,423 @@ const char *pa_status_string(int status) {
 }
 
 int pa_version(void) { return 100; }
+
+}  // extern "C"
+
+// ---------------------------------------------------------------- sliding window
+namespace pa {
+namespace {
+
+// Positions stay below 2^30 (the table's width is checked), so a longer
+// window or sink run means "all" and is cut to that.
+constexpr int32_t kWindowMax = 1 << 30;
+
+// Most blocks a call may have to read for one run of `queries` consecutive
+// query tokens: the sinks' and those any placement of the window touches.
+int64_t window_visible_blocks(int32_t max_blocks_per_seq, int32_t queries, int32_t window,
+                              int32_t num_sinks) {
+    const int64_t w = ((int64_t)window + queries - 1 + 2 * (kBlock - 1)) / kBlock;
+    const int64_t k = ((int64_t)num_sinks + kBlock - 1) / kBlock;
+    return std::min<int64_t>(max_blocks_per_seq, w + k);
+}
+
+// Blocks per partition of a windowed decode (see decode_window_kernel):
+// PA_PARTITION_TOKENS, but shorter while the grid would leave resident CTA
+// slots of the GPU (148 SMs x 6 CTAs) empty.
+constexpr int kWindowFill = 148 * PA_DECODE_MIN_CTAS;
+int window_part_blocks(int64_t seq_heads, int64_t visible) {
+    int pb = kPartBlocks;
+    while (pb > 8 && seq_heads * ((visible + pb - 1) / pb) < kWindowFill) pb /= 2;
+    return pb;
+}
+
+// Rows of a kv head (query tokens x group) up to which a chunk runs on
+// decode_window_kernel.
+constexpr int kChunkRows = 16;
+
+struct PrefillSplit {
+    int splits, split_tiles;
+};
+
+// Key-tile ranges per work item of a windowed prefill.
+PrefillSplit prefill_split(int32_t num_seqs, int32_t max_query_len, int32_t num_q_heads,
+                           int32_t num_kv_heads, int32_t max_blocks_per_seq, int32_t window,
+                           int32_t num_sinks) {
+    constexpr int kSms = 148, kMinTiles = 2;
+    const int group = num_q_heads / num_kv_heads;
+    const int tile_tokens = kUmmaQTiles * (kUmmaRows / group);
+    const int64_t items = (int64_t)num_seqs * num_kv_heads *
+                          ((max_query_len + tile_tokens - 1) / tile_tokens);
+    const int64_t blocks = window_visible_blocks(
+        max_blocks_per_seq, std::min(max_query_len, tile_tokens), window, num_sinks);
+    const int64_t tiles = (blocks + 7) / 8;
+    int64_t splits = std::min<int64_t>(std::max<int64_t>(kSms / items, 1), (tiles + kMinTiles - 1) / kMinTiles);
+    PrefillSplit r;
+    r.split_tiles = (int)((tiles + splits - 1) / splits);
+    r.splits = (int)((tiles + r.split_tiles - 1) / r.split_tiles);
+    return r;
+}
+
+template <typename T, int D, int NT, int PB, bool CHUNK>
+int launch_window_kernel(const WindowArgs &a, const CUtensorMap &tmk, const CUtensorMap &tmv,
+                         cudaStream_t st) {
+    constexpr int STAGES = D == 128 ? kStages128 : kStages64;
+    constexpr int SMEM = kWarps * STAGES * WarpPipe<D, STAGES>::kStage + 1024;
+    const dim3 grid(a.d.num_seqs * a.d.num_kv_heads, a.d.num_parts);
+    auto k = decode_window_kernel<T, D, kWarps, STAGES, NT, PB, CHUNK>;
+    if (!set_smem(k, SMEM)) return PA_ERR_CUDA;
+    return launch_pdl(k, grid, dim3(kWarps * 32), SMEM, st, tmk, tmv, a);
+}
+
+template <typename T, int D, bool CHUNK>
+int launch_window_merge(const WindowArgs &a, cudaStream_t st) {
+    const int64_t rows = (int64_t)a.d.num_seqs * a.max_query_len * a.d.num_q_heads;
+    return launch_pdl(merge_window_kernel<T, D, CHUNK>,
+                      dim3((unsigned)((rows + kMergeRows - 1) / kMergeRows)), dim3(kMergeRows * 32),
+                      0, st, a);
+}
+
+template <typename T, int D, bool CHUNK>
+int launch_window(const WindowArgs &a, const CUtensorMap &tmk, const CUtensorMap &tmv,
+                  cudaStream_t st) {
+    const int rows = a.max_query_len * (a.d.num_q_heads / a.d.num_kv_heads);
+    auto with_pb = [&](auto nt) -> int {
+        constexpr int NT = decltype(nt)::value;
+        switch (a.d.part_blocks) {
+            case 8: return launch_window_kernel<T, D, NT, 8, CHUNK>(a, tmk, tmv, st);
+            case 16: return launch_window_kernel<T, D, NT, 16, CHUNK>(a, tmk, tmv, st);
+            default: return launch_window_kernel<T, D, NT, kPartBlocks, CHUNK>(a, tmk, tmv, st);
+        }
+    };
+    const int rc = rows <= 8 ? with_pb(std::integral_constant<int, 1>{})
+                             : with_pb(std::integral_constant<int, 2>{});
+    if (rc != PA_OK || a.d.num_parts <= 1) return rc;
+    return launch_window_merge<T, D, CHUNK>(a, st);
+}
+
+// Workspace of a windowed call: `rows` query rows (token x head), `parts`
+// partitions each; nothing when no row can be split.
+size_t window_workspace(int64_t rows, int64_t head_dim, int64_t parts) {
+    return parts <= 1 ? 0 : (size_t)workspace_layout(1, rows, head_dim, parts).total;
+}
+
+int take_workspace(DecodeArgs &a, int64_t rows, int64_t head_dim, void *workspace,
+                   size_t workspace_bytes) {
+    a.ws_o = nullptr;
+    a.ws_ml = nullptr;
+    if (a.num_parts <= 1) return PA_OK;
+    const WorkspaceLayout l = workspace_layout(1, rows, head_dim, a.num_parts);
+    if (!workspace || workspace_bytes < (size_t)l.total || !aligned(workspace, 256))
+        return PA_ERR_WORKSPACE;
+    char *base = static_cast<char *>(workspace);
+    a.ws_o = reinterpret_cast<float *>(base + l.o_off);
+    a.ws_ml = reinterpret_cast<float2 *>(base + l.ml_off);
+    return PA_OK;
+}
+
+// Checks shared by the windowed calls, after check_cache_shape's and the
+// pointers' own.
+int check_window(int32_t window, int32_t num_sinks, int32_t max_blocks_per_seq) {
+    if (window < 1 || num_sinks < 0) return PA_ERR_INVALID_ARG;
+    if (max_blocks_per_seq > kWindowMax / kBlock) return PA_ERR_UNSUPPORTED;
+    return PA_OK;
+}
+
+template <bool CHUNK>
+int window_call(WindowArgs &a, int32_t head_dim, int32_t dtype, const void *key_cache,
+                const void *value_cache, cudaStream_t st) {
+    CUtensorMap tmk, tmv;
+    const DecodeArgs &d = a.d;
+    if (!encode_cache_map(&tmk, key_cache, d.num_blocks, d.num_kv_heads, head_dim, dtype) ||
+        !encode_cache_map(&tmv, value_cache, d.num_blocks, d.num_kv_heads, head_dim, dtype))
+        return PA_ERR_CUDA;
+    if (dtype == PA_F16)
+        return head_dim == 128 ? launch_window<__half, 128, CHUNK>(a, tmk, tmv, st)
+                               : launch_window<__half, 64, CHUNK>(a, tmk, tmv, st);
+    return head_dim == 128 ? launch_window<__nv_bfloat16, 128, CHUNK>(a, tmk, tmv, st)
+                           : launch_window<__nv_bfloat16, 64, CHUNK>(a, tmk, tmv, st);
+}
+
+int decode_window_call(void *out, const void *q, const void *k_new, const void *v_new,
+                       void *key_cache, void *value_cache, const int32_t *block_tables,
+                       const int32_t *context_lens, int32_t window, int32_t num_sinks,
+                       int32_t num_kv_heads, float scale, int32_t num_seqs, int32_t num_q_heads,
+                       int32_t head_dim, int32_t block_size, int32_t max_blocks_per_seq,
+                       int64_t num_blocks, int32_t dtype, void *workspace, size_t workspace_bytes,
+                       bool append, void *stream) {
+    bool empty = false;
+    int rc = check_decode_args(out, q, key_cache, value_cache, block_tables, context_lens,
+                               num_kv_heads, num_seqs, num_q_heads, head_dim, block_size,
+                               max_blocks_per_seq, num_blocks, dtype, &empty);
+    if (rc != PA_OK) return rc;
+    rc = check_window(window, num_sinks, max_blocks_per_seq);
+    if (rc != PA_OK || empty) return rc;
+    if (!aligned(q, 16) || !aligned(out, 16)) return PA_ERR_INVALID_ARG;
+    if (append && (!k_new || !v_new || !aligned(k_new, 16) || !aligned(v_new, 16)))
+        return PA_ERR_INVALID_ARG;
+    window = std::min(window, kWindowMax);
+    num_sinks = std::min(num_sinks, kWindowMax);
+    const int64_t visible = window_visible_blocks(max_blocks_per_seq, 1, window, num_sinks);
+    WindowArgs a = {};
+    a.d.out = out;
+    a.d.q = q;
+    a.d.block_tables = block_tables;
+    a.d.context_lens = context_lens;
+    a.d.num_blocks = num_blocks;
+    a.d.num_seqs = num_seqs;
+    a.d.num_q_heads = num_q_heads;
+    a.d.num_kv_heads = num_kv_heads;
+    a.d.max_blocks_per_seq = max_blocks_per_seq;
+    a.d.part_blocks = window_part_blocks((int64_t)num_seqs * num_kv_heads, visible);
+    const int64_t parts = (visible + a.d.part_blocks - 1) / a.d.part_blocks;
+    if (parts > 65535) return PA_ERR_UNSUPPORTED;
+    a.d.num_parts = (int)parts;
+    a.d.scale_log2 = scale * 1.4426950408889634f;
+    a.d.k_new = append ? k_new : nullptr;
+    a.d.v_new = append ? v_new : nullptr;
+    a.d.key_cache = key_cache;
+    a.d.value_cache = value_cache;
+    a.max_query_len = 1;
+    a.tile_tokens = 1;
+    a.window = window;
+    a.num_sinks = num_sinks;
+    rc = take_workspace(a.d, (int64_t)num_seqs * num_q_heads, head_dim, workspace, workspace_bytes);
+    if (rc != PA_OK) return rc;
+    return window_call<false>(a, head_dim, dtype, key_cache, value_cache,
+                              static_cast<cudaStream_t>(stream));
+}
+
+// Partitions (decode_window_kernel) or splits (prefill_umma_kernel) per row.
+int64_t prefill_window_parts(int32_t num_seqs, int32_t max_query_len, int32_t num_q_heads,
+                             int32_t num_kv_heads, int32_t max_blocks_per_seq, int32_t window,
+                             int32_t num_sinks, bool *rows_fit, int *part_blocks) {
+    const int group = num_q_heads / num_kv_heads;
+    *rows_fit = (int64_t)max_query_len * group <= kChunkRows;
+    if (*rows_fit) {
+        const int64_t visible =
+            window_visible_blocks(max_blocks_per_seq, max_query_len, window, num_sinks);
+        *part_blocks = window_part_blocks((int64_t)num_seqs * num_kv_heads, visible);
+        return (visible + *part_blocks - 1) / *part_blocks;
+    }
+    const PrefillSplit sp = prefill_split(num_seqs, max_query_len, num_q_heads, num_kv_heads,
+                                          max_blocks_per_seq, window, num_sinks);
+    *part_blocks = sp.split_tiles * (kUmmaKeys / kBlock);
+    return sp.splits;
+}
+
+}  // namespace
+}  // namespace pa
+
+extern "C" {
+
+size_t pa_decode_window_workspace_size(int32_t num_seqs, int32_t num_q_heads, int32_t num_kv_heads,
+                                       int32_t head_dim, int32_t block_size,
+                                       int32_t max_blocks_per_seq, int32_t window,
+                                       int32_t num_sinks) {
+    if (num_seqs <= 0 || num_q_heads <= 0 || num_kv_heads <= 0 || head_dim <= 0 ||
+        block_size != kBlock || max_blocks_per_seq <= 0 || window < 1 || num_sinks < 0)
+        return 0;
+    const int64_t visible = window_visible_blocks(max_blocks_per_seq, 1, window, num_sinks);
+    const int pb = window_part_blocks((int64_t)num_seqs * num_kv_heads, visible);
+    return window_workspace((int64_t)num_seqs * num_q_heads, head_dim, (visible + pb - 1) / pb);
+}
+
+int pa_decode_window(void *out, const void *q, const void *key_cache, const void *value_cache,
+                     const int32_t *block_tables, const int32_t *context_lens, int32_t window,
+                     int32_t num_sinks, int32_t num_kv_heads, float scale, int32_t num_seqs,
+                     int32_t num_q_heads, int32_t head_dim, int32_t block_size,
+                     int32_t max_blocks_per_seq, int64_t num_blocks, int32_t dtype,
+                     void *workspace, size_t workspace_bytes, void *stream) {
+    return decode_window_call(out, q, nullptr, nullptr, const_cast<void *>(key_cache),
+                              const_cast<void *>(value_cache), block_tables, context_lens, window,
+                              num_sinks, num_kv_heads, scale, num_seqs, num_q_heads, head_dim,
+                              block_size, max_blocks_per_seq, num_blocks, dtype, workspace,
+                              workspace_bytes, false, stream);
+}
+
+int pa_decode_append_window(void *out, const void *q, const void *k_new, const void *v_new,
+                            void *key_cache, void *value_cache, const int32_t *block_tables,
+                            const int32_t *context_lens, int32_t window, int32_t num_sinks,
+                            int32_t num_kv_heads, float scale, int32_t num_seqs,
+                            int32_t num_q_heads, int32_t head_dim, int32_t block_size,
+                            int32_t max_blocks_per_seq, int64_t num_blocks, int32_t dtype,
+                            void *workspace, size_t workspace_bytes, void *stream) {
+    return decode_window_call(out, q, k_new, v_new, key_cache, value_cache, block_tables,
+                              context_lens, window, num_sinks, num_kv_heads, scale, num_seqs,
+                              num_q_heads, head_dim, block_size, max_blocks_per_seq, num_blocks,
+                              dtype, workspace, workspace_bytes, true, stream);
+}
+
+size_t pa_prefill_window_workspace_size(int32_t num_seqs, int32_t num_q_tokens,
+                                        int32_t max_query_len, int32_t num_q_heads,
+                                        int32_t num_kv_heads, int32_t head_dim, int32_t block_size,
+                                        int32_t max_blocks_per_seq, int32_t window,
+                                        int32_t num_sinks) {
+    if (num_seqs <= 0 || num_q_tokens <= 0 || max_query_len <= 0 || num_kv_heads <= 0 ||
+        num_q_heads < num_kv_heads || num_q_heads / num_kv_heads > kUmmaRows || head_dim <= 0 ||
+        block_size != kBlock || max_blocks_per_seq <= 0 || window < 1 || num_sinks < 0)
+        return 0;
+    max_query_len = std::min(max_query_len, num_q_tokens);
+    bool rows_fit;
+    int pb;
+    const int64_t parts = prefill_window_parts(num_seqs, max_query_len, num_q_heads, num_kv_heads,
+                                               max_blocks_per_seq, window, num_sinks, &rows_fit, &pb);
+    return window_workspace((int64_t)num_q_tokens * num_q_heads, head_dim, parts);
+}
+
+int pa_prefill_window(void *out, const void *q, const void *key_cache, const void *value_cache,
+                      const int32_t *block_tables, const int32_t *context_lens,
+                      const int32_t *query_start, int32_t max_query_len, int32_t window,
+                      int32_t num_sinks, int32_t num_kv_heads, float scale, int32_t num_seqs,
+                      int32_t num_q_heads, int32_t num_q_tokens, int32_t head_dim,
+                      int32_t block_size, int32_t max_blocks_per_seq, int64_t num_blocks,
+                      int32_t dtype, void *workspace, size_t workspace_bytes, void *stream) {
+    int rc = check_cache_shape(num_kv_heads, head_dim, block_size, num_blocks, dtype);
+    if (rc != PA_OK) return rc;
+    if (num_seqs < 0 || num_q_heads <= 0 || num_q_tokens < 0 || max_query_len < 0 ||
+        max_blocks_per_seq <= 0)
+        return PA_ERR_INVALID_ARG;
+    if (num_q_heads % num_kv_heads != 0) return PA_ERR_INVALID_ARG;
+    rc = check_window(window, num_sinks, max_blocks_per_seq);
+    if (rc != PA_OK) return rc;
+    const int group = num_q_heads / num_kv_heads;
+    if (group > kUmmaRows || !(scale > 0.f && scale < 3.0e38f)) return PA_ERR_UNSUPPORTED;
+    if (num_seqs == 0 || num_q_tokens == 0 || max_query_len == 0) return PA_OK;
+    if (!out || !q || !key_cache || !value_cache || !block_tables || !context_lens || !query_start)
+        return PA_ERR_INVALID_ARG;
+    if (!aligned(key_cache, 16) || !aligned(value_cache, 16) || !aligned(q, 16) ||
+        !aligned(out, 16) || !aligned(block_tables, 4) || !aligned(context_lens, 4) ||
+        !aligned(query_start, 4))
+        return PA_ERR_INVALID_ARG;
+    max_query_len = std::min(max_query_len, num_q_tokens);
+    if ((int64_t)num_seqs * num_kv_heads >= (int64_t(1) << 31) ||
+        (int64_t)num_seqs * max_query_len >= (int64_t(1) << 33) / num_q_heads)
+        return PA_ERR_UNSUPPORTED;
+    window = std::min(window, kWindowMax);
+    num_sinks = std::min(num_sinks, kWindowMax);
+
+    bool rows_fit;
+    WindowArgs a = {};
+    const int64_t parts = prefill_window_parts(num_seqs, max_query_len, num_q_heads, num_kv_heads,
+                                               max_blocks_per_seq, window, num_sinks, &rows_fit,
+                                               &a.d.part_blocks);
+    if (parts > 65535) return PA_ERR_UNSUPPORTED;
+    a.d.out = out;
+    a.d.q = q;
+    a.d.block_tables = block_tables;
+    a.d.context_lens = context_lens;
+    a.d.num_blocks = num_blocks;
+    a.d.num_seqs = num_seqs;
+    a.d.num_q_heads = num_q_heads;
+    a.d.num_kv_heads = num_kv_heads;
+    a.d.max_blocks_per_seq = max_blocks_per_seq;
+    a.d.num_parts = (int)parts;
+    a.d.scale_log2 = scale * 1.4426950408889634f;
+    a.query_start = query_start;
+    a.num_q_tokens = num_q_tokens;
+    a.max_query_len = max_query_len;
+    a.tile_tokens = rows_fit ? max_query_len : kUmmaQTiles * (kUmmaRows / group);
+    a.window = window;
+    a.num_sinks = num_sinks;
+    rc = take_workspace(a.d, (int64_t)num_q_tokens * num_q_heads, head_dim, workspace,
+                        workspace_bytes);
+    if (rc != PA_OK) return rc;
+    cudaStream_t st = static_cast<cudaStream_t>(stream);
+    if (rows_fit) return window_call<true>(a, head_dim, dtype, key_cache, value_cache, st);
+
+    PrefillWindow pw;
+    pw.window = window;
+    pw.num_sinks = num_sinks;
+    pw.max_query_len = max_query_len;
+    pw.splits = (int)parts;
+    pw.split_tiles = a.d.part_blocks / (kUmmaKeys / kBlock);
+    pw.ws_o = a.d.ws_o;
+    pw.ws_ml = a.d.ws_ml;
+    rc = launch_prefill_umma(out, q, key_cache, value_cache, block_tables, context_lens,
+                             query_start, max_query_len, num_kv_heads, scale, num_seqs,
+                             num_q_heads, num_q_tokens, head_dim, max_blocks_per_seq, num_blocks,
+                             dtype, &pw, st);
+    if (rc != PA_OK || parts <= 1) return rc;
+    if (dtype == PA_F16)
+        return head_dim == 128 ? launch_window_merge<__half, 128, true>(a, st)
+                               : launch_window_merge<__half, 64, true>(a, st);
+    return head_dim == 128 ? launch_window_merge<__nv_bfloat16, 128, true>(a, st)
+                           : launch_window_merge<__nv_bfloat16, 64, true>(a, st);
+}
+
+// ---------------------------------------------------------------- rotary positions
+int pa_rope_init(pa_rope *rope, const float *inv_freq, const int32_t *pair_axes, int32_t num_pairs,
+                 int32_t num_axes, int32_t interleaved) {
+    if (!rope || num_pairs <= 0 || num_axes <= 0 || !inv_freq) return PA_ERR_INVALID_ARG;
+    if (num_pairs > PA_ROPE_MAX_PAIRS || num_pairs % 8 != 0 || num_axes > PA_ROPE_MAX_AXES)
+        return PA_ERR_UNSUPPORTED;
+    pa_rope r = {};
+    for (int32_t i = 0; i < num_pairs; ++i) {
+        const int32_t axis = pair_axes ? pair_axes[i] : 0;
+        if (axis < 0 || axis >= num_axes || !std::isfinite(inv_freq[i])) return PA_ERR_INVALID_ARG;
+        // the angle of one position step in turns, modulo a whole turn, as a
+        // 64-bit fraction: long double keeps 64 bits of the quotient
+        const long double turns = (long double)inv_freq[i] / 6.28318530717958647692528676655900577L;
+        long double frac = turns - std::floor(turns);
+        r.turns[i] = frac >= 1.0L ? 0 : (uint64_t)(frac * 18446744073709551616.0L);
+        r.axis[i] = (uint8_t)axis;
+    }
+    r.num_pairs = num_pairs;
+    r.num_axes = num_axes;
+    r.interleaved = interleaved != 0;
+    *rope = r;
+    return PA_OK;
+}
+
+int pa_rope_and_cache(void *q_out, const void *q, const void *k, const void *v, void *key_cache,
+                      void *value_cache, const int64_t *slot_mapping, const int32_t *positions,
+                      const pa_rope *rope, int64_t q_stride, int64_t k_stride, int64_t v_stride,
+                      int32_t num_tokens, int32_t num_q_heads, int32_t num_kv_heads,
+                      int32_t head_dim, int32_t block_size, int64_t num_blocks, int32_t dtype,
+                      void *stream) {
+    int rc = check_cache_shape(num_kv_heads, head_dim, block_size, num_blocks, dtype);
+    if (rc != PA_OK) return rc;
+    if (!rope || num_tokens < 0 || num_q_heads < 0 || q_stride < 0 || k_stride < 0 || v_stride < 0)
+        return PA_ERR_INVALID_ARG;
+    if (rope->num_pairs <= 0 || rope->num_pairs % 8 != 0 || 2 * rope->num_pairs > head_dim ||
+        rope->num_axes <= 0 || rope->num_axes > PA_ROPE_MAX_AXES)
+        return PA_ERR_INVALID_ARG;
+    for (int32_t i = 0; i < rope->num_pairs; ++i)
+        if (rope->axis[i] >= rope->num_axes) return PA_ERR_INVALID_ARG;
+    if (num_tokens == 0) return PA_OK;
+    if ((num_q_heads > 0 && (!q || !q_out)) || !k || !v || !key_cache || !value_cache ||
+        !slot_mapping || !positions)
+        return PA_ERR_INVALID_ARG;
+    if (!aligned(q, 16) || !aligned(q_out, 16) || !aligned(k, 16) || !aligned(v, 16) ||
+        !aligned(key_cache, 16) || !aligned(value_cache, 16) || !aligned(slot_mapping, 8) ||
+        !aligned(positions, 4) || q_stride % 8 != 0 || k_stride % 8 != 0 || v_stride % 8 != 0)
+        return PA_ERR_INVALID_ARG;
+    if ((int64_t)num_q_heads + 2 * (int64_t)num_kv_heads > (1 << 24)) return PA_ERR_UNSUPPORTED;
+    RopeArgs a;
+    a.q_out = static_cast<uint4 *>(q_out);
+    a.q = static_cast<const uint4 *>(q);
+    a.k = static_cast<const uint4 *>(k);
+    a.v = static_cast<const uint4 *>(v);
+    a.key_cache = static_cast<uint4 *>(key_cache);
+    a.value_cache = static_cast<uint4 *>(value_cache);
+    a.slots = slot_mapping;
+    a.positions = positions;
+    a.q_stride = q_stride / 8;
+    a.k_stride = k_stride / 8;
+    a.v_stride = v_stride / 8;
+    a.num_slots = num_blocks * kBlock;
+    a.num_tokens = num_tokens;
+    a.num_q_heads = num_q_heads;
+    a.num_kv_heads = num_kv_heads;
+    a.rope = *rope;
+    cudaStream_t st = static_cast<cudaStream_t>(stream);
+    const dim3 grid(num_tokens), block(kRopeThreads);
+    auto launch = [&](auto kernel) { return launch_pdl(kernel, grid, block, 0, st, a); };
+    if (dtype == PA_F16)
+        return head_dim == 128 ? launch(rope_kernel<__half, 128>) : launch(rope_kernel<__half, 64>);
+    return head_dim == 128 ? launch(rope_kernel<__nv_bfloat16, 128>)
+                           : launch(rope_kernel<__nv_bfloat16, 64>);
+}
 
 }  // extern "C"
 

@@ -676,17 +676,7 @@ constexpr int kMergeRows = 4;
 constexpr int kMergeFew = 8;  // rows of at most this many partitions load everything at once
 
 template <typename T, int D>
-__global__ void __launch_bounds__(kMergeRows * 32) merge_kernel(const DecodeArgs a) {
-    pdl_launch_dependents();
-    pdl_wait_prior();
-    const int lane = threadIdx.x & 31;
-    const size_t row = (size_t)blockIdx.x * kMergeRows + (threadIdx.x >> 5);
-    if (row >= (size_t)a.num_seqs * a.num_q_heads) return;
-    const int s = (int)(row / a.num_q_heads);
-    const int L = clamp_context(a, s, false);
-    const int nblk = (L + kBlock - 1) / kBlock;
-    const int nparts = (nblk + a.part_blocks - 1) / a.part_blocks;
-    if (nparts <= 1) return;
+__device__ __forceinline__ void merge_row(const DecodeArgs &a, size_t row, int nparts, int lane) {
     const float2 *ml = a.ws_ml + row * a.num_parts;
     constexpr int D4 = D / 4;  // float4 pieces of a row
     const float4 *op = reinterpret_cast<const float4 *>(a.ws_o + row * a.num_parts * D);
@@ -755,6 +745,21 @@ __global__ void __launch_bounds__(kMergeRows * 32) merge_kernel(const DecodeArgs
         const uint32_t hi = (uint32_t)narrow1(acc.z * inv, T()) | ((uint32_t)narrow1(acc.w * inv, T()) << 16);
         *reinterpret_cast<uint2 *>(out) = make_uint2(lo, hi);
     }
+}
+
+template <typename T, int D>
+__global__ void __launch_bounds__(kMergeRows * 32) merge_kernel(const DecodeArgs a) {
+    pdl_launch_dependents();
+    pdl_wait_prior();
+    const int lane = threadIdx.x & 31;
+    const size_t row = (size_t)blockIdx.x * kMergeRows + (threadIdx.x >> 5);
+    if (row >= (size_t)a.num_seqs * a.num_q_heads) return;
+    const int s = (int)(row / a.num_q_heads);
+    const int L = clamp_context(a, s, false);
+    const int nblk = (L + kBlock - 1) / kBlock;
+    const int nparts = (nblk + a.part_blocks - 1) / a.part_blocks;
+    if (nparts <= 1) return;
+    merge_row<T, D>(a, row, nparts, lane);
 }
 
 // ------------------------------------------------------------------ scatter write

@@ -41,6 +41,13 @@
 //
 // Shared-memory tiles are stacks of 8-row x 128-byte atoms in the TMA
 // 128-byte swizzle; a 128-row tile of D columns is D / 64 chunks of 16 KiB.
+// WIN builds (pa_prefill_window) walk the blocks that some row of the item
+// sees instead of the whole context: the sink blocks, then the window's,
+// packed into key tiles without a gap (a tile is gathered block by block
+// anyway), and mask each row to its own window.  With few items the tiles of
+// an item are split over several CTAs (w.splits); each writes its normalised
+// O, max and sum to the workspace and merge_window_kernel joins them.
+//
 // Warp 11 only completes the third warpgroup (setmaxnreg works per
 // warpgroup).  Every wait is bounded; a wait that gives up raises the CTA's abort flag, the
 // other roles leave their loops, in-flight copies and MMAs are waited for,
@@ -50,6 +57,7 @@
 #include "pa_exp2.cuh"
 #include "pa_kernels.cuh"
 #include "pa_umma.cuh"
+#include "pa_window.cuh"
 
 namespace pa {
 
@@ -122,12 +130,30 @@ __device__ __forceinline__ bool wait_or_abort(uint64_t *bar, uint32_t parity,
 struct UmmaItem {
     int s, kvh, tile, q0, n, L, row0, rows_total, nkeys, nblk, ntiles;
     const int32_t *trow;
+    // WIN: first key tile and index of this split, splits with tiles, and the
+    // visible blocks (nblk counts those)
+    int t0, part, nparts;
+    WindowSeq w;
+};
+
+// Window of a pa_prefill_window call (unused otherwise).
+struct PrefillWindow {
+    int window, num_sinks, max_query_len;
+    int splits, split_tiles;  // key-tile ranges per item, tiles in each
+    float *ws_o;              // [num_q_tokens][Hq][splits][D]
+    float2 *ws_ml;            // [num_q_tokens][Hq][splits]
 };
 
 // Item i; false when it has no rows (a sequence with fewer query tokens than
 // the grid was sized for) or invalid bounds (reported by `report`).
-__device__ __forceinline__ bool umma_item(const PrefillArgs &a, const int *s_order, int i, int G,
-                                          int rows_used, bool report, UmmaItem &it) {
+template <bool WIN>
+__device__ __forceinline__ bool umma_item(const PrefillArgs &a, const PrefillWindow &pw,
+                                          const int *s_order, int i, int G, int rows_used,
+                                          bool report, UmmaItem &it) {
+    if constexpr (WIN) {
+        it.part = i % pw.splits;
+        i /= pw.splits;
+    }
     const int per_seq = a.tiles_per_seq * a.num_kv_heads;
     const int rank = i / per_seq, rem = i % per_seq;
     it.tile = a.tiles_per_seq - 1 - rem / a.num_kv_heads;
@@ -147,6 +173,12 @@ __device__ __forceinline__ bool umma_item(const PrefillArgs &a, const int *s_ord
         L = L < 0 ? 0 : (L > cap ? cap : L);
         n = n < 0 ? 0 : (n > L ? L : n);
     }
+    if constexpr (WIN) {
+        if (n > pw.max_query_len) {
+            if (report && head && it.part == 0) flag_error(PA_DEVERR_CONTEXT_LEN);
+            return false;
+        }
+    }
     it.n = n;
     it.L = L;
     it.rows_total = n * G;
@@ -156,6 +188,15 @@ __device__ __forceinline__ bool umma_item(const PrefillArgs &a, const int *s_ord
     it.nkeys = L - n + last_row / G + 1;
     it.nblk = (it.nkeys + kBlock - 1) / kBlock;
     it.ntiles = (it.nkeys + kUmmaKeys - 1) / kUmmaKeys;
+    if constexpr (WIN) {
+        window_blocks(it.w, L - n + it.row0 / G, it.nkeys, pw.window, pw.num_sinks);
+        it.nblk = it.w.nv;
+        const int tiles = (it.nblk + kUmmaKeys / kBlock - 1) / (kUmmaKeys / kBlock);
+        it.nparts = (tiles + pw.split_tiles - 1) / pw.split_tiles;
+        if (it.part >= it.nparts) return false;
+        it.t0 = it.part * pw.split_tiles;
+        it.ntiles = min(pw.split_tiles, tiles - it.t0);
+    }
     it.trow = a.block_tables + (size_t)it.s * a.max_blocks_per_seq;
     return true;
 }
@@ -168,11 +209,12 @@ __device__ __forceinline__ int umma_round_item(int r) {
     return r * P + ((r & 1) ? P - 1 - c : c);
 }
 
-template <typename T, int D>
+template <typename T, int D, bool WIN>
 __global__ void __launch_bounds__(kUmmaThreads, 1)
     prefill_umma_kernel(const __grid_constant__ CUtensorMap tmq,
                         const __grid_constant__ CUtensorMap tmk,
-                        const __grid_constant__ CUtensorMap tmv, const PrefillArgs a) {
+                        const __grid_constant__ CUtensorMap tmv, const PrefillArgs a,
+                        const PrefillWindow pw) {
     static_assert(D == 64 || D == 128, "head dim");
     constexpr int NCH = D / 64;                   // 128-byte chunks per row
     constexpr int QB = kUmmaRows * D * 2;         // one query tile
@@ -200,7 +242,7 @@ __global__ void __launch_bounds__(kUmmaThreads, 1)
     const int G = a.num_q_heads / a.num_kv_heads;
     const int TT = kUmmaRows / G, rows_used = TT * G;  // query tokens / rows per query tile
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    const int total = a.num_seqs * a.tiles_per_seq * a.num_kv_heads;
+    const int total = a.num_seqs * a.tiles_per_seq * a.num_kv_heads * (WIN ? pw.splits : 1);
     pdl_launch_dependents();
     pdl_wait_prior();
     if (warp == 8 && lane == 0) {
@@ -255,7 +297,7 @@ __global__ void __launch_bounds__(kUmmaThreads, 1)
             const int i = umma_round_item(r);
             if (i >= total) break;
             UmmaItem it;
-            if (!umma_item(a, s_order, i, G, rows_used, is_k && lane == 0, it)) continue;
+            if (!umma_item<WIN>(a, pw, s_order, i, G, rows_used, is_k && lane == 0, it)) continue;
             if (is_k) {
                 bool freed = true;
                 if (lane == 0) {
@@ -277,10 +319,10 @@ __global__ void __launch_bounds__(kUmmaThreads, 1)
             for (int j = 0; j < it.ntiles; ++j) {
                 const int g = gt + j, st = g & 1;
                 const uint32_t ph = (g >> 1) & 1;
-                const int blk = j * 8 + bi;
+                const int blk = (WIN ? it.t0 + j : j) * 8 + bi;
                 int id = -1;
                 if (lane < BOXES && blk < it.nblk) {
-                    id = it.trow[blk];
+                    id = it.trow[WIN ? it.w.block(blk) : blk];
                     if (id < 0 || id >= a.num_blocks) {
                         flag_error(PA_DEVERR_BLOCK_ID);
                         id = -1;
@@ -345,7 +387,7 @@ __global__ void __launch_bounds__(kUmmaThreads, 1)
                 const int i = umma_round_item(r);
                 if (i >= total) break;
                 UmmaItem it;
-                if (!umma_item(a, s_order, i, G, rows_used, false, it)) continue;
+                if (!umma_item<WIN>(a, pw, s_order, i, G, rows_used, false, it)) continue;
                 if (!(ok = wait_or_abort(q_full, items & 1, abort_flag) &&
                            wait_or_abort(&k_full[gt & 1], (gt >> 1) & 1, abort_flag)))
                     break;
@@ -410,7 +452,7 @@ __global__ void __launch_bounds__(kUmmaThreads, 1)
             const int i = umma_round_item(rr);
             if (i >= total) break;
             UmmaItem it;
-            if (!umma_item(a, s_order, i, G, rows_used, false, it)) continue;
+            if (!umma_item<WIN>(a, pw, s_order, i, G, rows_used, false, it)) continue;
             const int R = it.row0 + k * rows_used + r;
             const bool rvalid = r < rows_used && R < it.rows_total;
             const int qi = rvalid ? R / G : 0, qh = rvalid ? R % G : 0;
@@ -423,9 +465,9 @@ __global__ void __launch_bounds__(kUmmaThreads, 1)
                 uint32_t bad = 0;
 #pragma unroll
                 for (int q = 0; q < 8; ++q) {
-                    const int blk = j * 8 + q;
+                    const int blk = (WIN ? it.t0 + j : j) * 8 + q;
                     if (blk < it.nblk) {
-                        const int id = it.trow[blk];
+                        const int id = it.trow[WIN ? it.w.block(blk) : blk];
                         if (id < 0 || id >= a.num_blocks) bad |= 1u << q;
                     }
                 }
@@ -438,11 +480,37 @@ __global__ void __launch_bounds__(kUmmaThreads, 1)
                 uint32_t x[kUmmaKeys];
                 tmem_ld128(t_s, x);
 
-                const int key0 = j * kUmmaKeys;
+                // token of column c: key0 + c (WIN: of the columns from nsc on)
+                int key0 = j * kUmmaKeys;
+                int nsc = 0, vis_a = 0, vis_b = 0, vis_end = 0;
+                if constexpr (WIN) {
+                    // The first nsc columns hold sink blocks away from the window
+                    // (none of their tokens lies in it); this row sees columns
+                    // [0, vis_a) and [vis_b, vis_end).
+                    const int v0 = (it.t0 + j) * (kUmmaKeys / kBlock);
+                    key0 = (v0 + it.w.skip) * kBlock;
+                    vis_end = min(pos - key0 + 1, kUmmaKeys);
+                    if (it.w.skip > 0) {
+                        nsc = min(max((it.w.nsb - v0) * kBlock, 0), kUmmaKeys);
+                        vis_a = min(max(pw.num_sinks - v0 * kBlock, 0), nsc);
+                    } else {
+                        vis_a = min(max(pw.num_sinks - key0, 0), vis_end);
+                    }
+                    vis_b = max(nsc, pos - pw.window - key0 + 1);
+                }
                 // the max of the raw scores (scale > 0 keeps the order); three-input
                 // max, four independent chains
                 float mx4[4] = {kMaskedLogit, kMaskedLogit, kMaskedLogit, kMaskedLogit};
-                if (key0 + kUmmaKeys - 1 > pos || bad) {
+                if constexpr (WIN) {
+                    // -infinity: a row may see nothing of its first tiles
+                    if (vis_b > vis_a || vis_end < kUmmaKeys || bad) {
+#pragma unroll
+                        for (int c = 0; c < kUmmaKeys; ++c) {
+                            const bool seen = c < vis_a || (c >= vis_b && c < vis_end);
+                            if (!seen || ((bad >> (c >> 4)) & 1u)) x[c] = __float_as_uint(-INFINITY);
+                        }
+                    }
+                } else if (key0 + kUmmaKeys - 1 > pos || bad) {
 #pragma unroll
                     for (int c = 0; c < kUmmaKeys; ++c) {
                         const bool masked = key0 + c > pos || ((bad >> (c >> 4)) & 1u);
@@ -501,7 +569,11 @@ __global__ void __launch_bounds__(kUmmaThreads, 1)
                         tmem_st32(t_o + c0, o);
                     }
                 }
-                if (k == 0 && (key0 + kUmmaKeys > live_end || bad)) {
+                bool dead_rows = key0 + kUmmaKeys > live_end || bad;  // V rows without data
+                if constexpr (WIN)  // or that no row of the item sees
+                    dead_rows = key0 + kUmmaKeys > it.nkeys || bad || key0 + nsc < it.w.lo ||
+                                (nsc > 0 && vis_a < nsc);
+                if (k == 0 && dead_rows) {
                     // V rows without data (past the context, never loaded, bad
                     // block) meet P = 0 in the MMA; zero them so that whatever
                     // they hold cannot turn 0 * x into NaN
@@ -511,7 +583,11 @@ __global__ void __launch_bounds__(kUmmaThreads, 1)
                         break;
                     }
                     const int key = key0 + r;
-                    if (key >= live_end || ((bad >> (r >> 4)) & 1u)) {
+                    bool clear = key >= live_end;
+                    if constexpr (WIN)
+                        clear = r < nsc ? r >= vis_a
+                                        : key >= it.nkeys || (key < it.w.lo && key >= pw.num_sinks);
+                    if (clear || ((bad >> (r >> 4)) & 1u)) {
                         uint8_t *vrow = sv + (g & 1) * KVB + r * 128;
 #pragma unroll
                         for (int c = 0; c < NCH; ++c)
@@ -537,6 +613,31 @@ __global__ void __launch_bounds__(kUmmaThreads, 1)
             }
             tc_fence_after();
             const float inv = l > 0.f ? 1.f / l : 0.f;
+            if constexpr (WIN) {
+                if (it.nparts > 1) {  // one of several splits: its share to the workspace
+                    const size_t row = (size_t)(it.q0 + qi) * a.num_q_heads + (size_t)it.kvh * G + qh;
+                    float *wo = pw.ws_o + (row * pw.splits + it.part) * D;
+#pragma unroll
+                    for (int c0 = 0; c0 < D; c0 += 32) {
+                        uint32_t o[32];
+                        tmem_ld32(t_o + c0, o);
+                        if (rvalid) {
+#pragma unroll
+                            for (int u = 0; u < 8; ++u)
+                                *reinterpret_cast<float4 *>(wo + c0 + 4 * u) =
+                                    make_float4(__uint_as_float(o[4 * u]) * inv,
+                                                __uint_as_float(o[4 * u + 1]) * inv,
+                                                __uint_as_float(o[4 * u + 2]) * inv,
+                                                __uint_as_float(o[4 * u + 3]) * inv);
+                        }
+                    }
+                    if (rvalid) pw.ws_ml[row * pw.splits + it.part] = make_float2(m_run, l);
+                    tc_fence_before();
+                    gt += it.ntiles;
+                    ++items;
+                    continue;
+                }
+            }
             const bool out32 = (reinterpret_cast<uintptr_t>(a.out) & 31) == 0;
             uint16_t *orow = reinterpret_cast<uint16_t *>(a.out) +
                              ((size_t)(it.q0 + qi) * a.num_q_heads + (size_t)it.kvh * G + qh) * D;
