@@ -294,12 +294,22 @@ def prefill(out, q, key_cache, value_cache, block_tables, context_lens, query_st
 
 
 # ---------------------------------------------------------------- sliding window, rotary positions
-def _one_device(tensors):
-    """Every tensor on the current CUDA device (the launch goes there)."""
-    dev = _torch().cuda.current_device()
-    for t in tensors:
-        if t.get_device() != dev:
-            raise ValueError(f"every tensor must be on the current CUDA device {dev}, got {t.device}")
+# These calls end within a few microseconds on the GPU, so their checks are
+# kept to plain attribute reads and pass addresses as integers.
+def _ptr(t, name, dtype, dev):
+    """Address of a contiguous tensor of `dtype` on CUDA device `dev`."""
+    if t.dtype is not dtype or t.get_device() != dev or not t.is_contiguous():
+        _dev(t, name, dtype)
+        raise ValueError(f"{name} must be on the current CUDA device {dev}, got {t.device}")
+    return t.data_ptr()
+
+
+def _device_stream(stream):
+    """(current CUDA device, raw stream handle): the launch goes there."""
+    torch = _torch()
+    dev = torch.cuda.current_device()
+    # the handle alone: current_stream() builds a Stream object, over 1 us
+    return dev, torch._C._cuda_getCurrentRawStream(dev) if stream is None else stream.cuda_stream
 
 
 def _i32_arg(x, name):
@@ -309,25 +319,27 @@ def _i32_arg(x, name):
     return x
 
 
-def _workspace(workspace):
+def _workspace(workspace, dev):
     if workspace is None:
         return None, 0
-    _one_device((workspace,))
-    return _dev(workspace, "workspace"), workspace.numel() * workspace.element_size()
+    return _ptr(workspace, "workspace", workspace.dtype, dev), workspace.nbytes
 
 
 def _window_shapes(out, q, key_cache, value_cache, block_tables, context_lens, num_kv_heads):
-    """Shared checks of the windowed calls -> (num_blocks, d, block size, Hq)."""
-    nb, hkv, bs, d = _cache_shape(key_cache, value_cache)
+    """Shared checks of the windowed calls -> (rows, Hq, d, block size, num_blocks, S, max_blocks)."""
+    shape = key_cache.shape
+    nb, hkv, bs, d = shape
+    if value_cache.shape != shape:
+        raise ValueError("key_cache and value_cache must match")
     if hkv != num_kv_heads:
         raise ValueError("num_kv_heads does not match the cache")
     rows, hq, dq = q.shape
-    if dq != d or out.shape != q.shape or out.dtype != q.dtype or q.dtype != key_cache.dtype:
+    if dq != d or out.shape != q.shape:
         raise ValueError("q / out must be [rows, Hq, d] of the cache dtype")
-    S = context_lens.shape[0]
-    if block_tables.dim() != 2 or block_tables.shape[0] != S or context_lens.dim() != 1:
+    S, maxb = block_tables.shape
+    if context_lens.shape != (S,):
         raise ValueError("block_tables must be [S, max_blocks], context_lens [S]")
-    return nb, d, bs, hq
+    return rows, hq, d, bs, nb, S, maxb
 
 
 def decode_window_workspace_size(num_seqs: int, num_q_heads: int, num_kv_heads: int, head_dim: int,
@@ -344,47 +356,46 @@ def decode_window(out, q, key_cache, value_cache, block_tables, context_lens, nu
     """decode over a sliding window and the first tokens: the query at position
     p = context_lens[s] - 1 sees token j when p - j < window or j < num_sinks.
     Table entries of blocks without such a token are not read."""
-    torch = _torch()
-    nb, d, bs, hq = _window_shapes(out, q, key_cache, value_cache, block_tables, context_lens,
-                                   num_kv_heads)
-    S = q.shape[0]
-    if context_lens.shape[0] != S:
-        raise ValueError("context_lens must be [S]")
-    _one_device((out, q, key_cache, value_cache, block_tables, context_lens))
-    ws_ptr, ws_bytes = _workspace(workspace)
-    _check(pa_decode_window(_dev(out, "out"), _dev(q, "q"), _dev(key_cache, "key_cache"),
-                            _dev(value_cache, "value_cache"),
-                            _dev(block_tables, "block_tables", torch.int32),
-                            _dev(context_lens, "context_lens", torch.int32),
+    rows, hq, d, bs, nb, S, maxb = _window_shapes(out, q, key_cache, value_cache, block_tables,
+                                                  context_lens, num_kv_heads)
+    if rows != S:
+        raise ValueError("q must have one row per sequence")
+    dev, st = _device_stream(stream)
+    i32, dtype = _torch().int32, q.dtype
+    ws_ptr, ws_bytes = _workspace(workspace, dev)
+    _check(pa_decode_window(_ptr(out, "out", dtype, dev), _ptr(q, "q", dtype, dev),
+                            _ptr(key_cache, "key_cache", dtype, dev),
+                            _ptr(value_cache, "value_cache", dtype, dev),
+                            _ptr(block_tables, "block_tables", i32, dev),
+                            _ptr(context_lens, "context_lens", i32, dev),
                             _i32_arg(window, "window"), _i32_arg(num_sinks, "num_sinks"),
-                            num_kv_heads, float(scale), S, hq, d, bs, block_tables.shape[1], nb,
-                            dtype_code(q), ws_ptr, ws_bytes, _stream(stream)), "pa_decode_window")
+                            num_kv_heads, scale, S, hq, d, bs, maxb, nb, dtype_code(q), ws_ptr,
+                            ws_bytes, st), "pa_decode_window")
 
 
 def decode_append_window(out, q, k_new, v_new, key_cache, value_cache, block_tables, context_lens,
                          num_kv_heads: int, scale: float, window: int, num_sinks: int = 0,
                          workspace=None, stream=None):
     """decode_append over a sliding window and the first tokens (decode_window)."""
-    torch = _torch()
-    nb, d, bs, hq = _window_shapes(out, q, key_cache, value_cache, block_tables, context_lens,
-                                   num_kv_heads)
-    S = q.shape[0]
-    if context_lens.shape[0] != S:
-        raise ValueError("context_lens must be [S]")
-    for name, t in (("k_new", k_new), ("v_new", v_new)):
-        if tuple(t.shape) != (S, num_kv_heads, d) or t.dtype != key_cache.dtype:
-            raise ValueError(f"{name} must be [S, Hkv, d] of the cache dtype")
-    _one_device((out, q, k_new, v_new, key_cache, value_cache, block_tables, context_lens))
-    ws_ptr, ws_bytes = _workspace(workspace)
-    _check(pa_decode_append_window(_dev(out, "out"), _dev(q, "q"), _dev(k_new, "k_new"),
-                                   _dev(v_new, "v_new"), _dev(key_cache, "key_cache"),
-                                   _dev(value_cache, "value_cache"),
-                                   _dev(block_tables, "block_tables", torch.int32),
-                                   _dev(context_lens, "context_lens", torch.int32),
+    rows, hq, d, bs, nb, S, maxb = _window_shapes(out, q, key_cache, value_cache, block_tables,
+                                                  context_lens, num_kv_heads)
+    if rows != S:
+        raise ValueError("q must have one row per sequence")
+    if k_new.shape != (S, num_kv_heads, d) or v_new.shape != (S, num_kv_heads, d):
+        raise ValueError("k_new and v_new must be [S, Hkv, d] of the cache dtype")
+    dev, st = _device_stream(stream)
+    i32, dtype = _torch().int32, q.dtype
+    ws_ptr, ws_bytes = _workspace(workspace, dev)
+    _check(pa_decode_append_window(_ptr(out, "out", dtype, dev), _ptr(q, "q", dtype, dev),
+                                   _ptr(k_new, "k_new", dtype, dev),
+                                   _ptr(v_new, "v_new", dtype, dev),
+                                   _ptr(key_cache, "key_cache", dtype, dev),
+                                   _ptr(value_cache, "value_cache", dtype, dev),
+                                   _ptr(block_tables, "block_tables", i32, dev),
+                                   _ptr(context_lens, "context_lens", i32, dev),
                                    _i32_arg(window, "window"), _i32_arg(num_sinks, "num_sinks"),
-                                   num_kv_heads, float(scale), S, hq, d, bs,
-                                   block_tables.shape[1], nb, dtype_code(q), ws_ptr, ws_bytes,
-                                   _stream(stream)), "pa_decode_append_window")
+                                   num_kv_heads, scale, S, hq, d, bs, maxb, nb, dtype_code(q),
+                                   ws_ptr, ws_bytes, st), "pa_decode_append_window")
 
 
 def prefill_window_workspace_size(num_seqs: int, num_q_tokens: int, max_query_len: int,
@@ -402,23 +413,23 @@ def prefill_window(out, q, key_cache, value_cache, block_tables, context_lens, q
                    num_sinks: int = 0, workspace=None, stream=None):
     """Chunked prefill over a sliding window and the first tokens: the row at
     position p sees token j when j <= p and (p - j < window or j < num_sinks)."""
-    torch = _torch()
-    nb, d, bs, hq = _window_shapes(out, q, key_cache, value_cache, block_tables, context_lens,
-                                   num_kv_heads)
-    S = context_lens.shape[0]
+    rows, hq, d, bs, nb, S, maxb = _window_shapes(out, q, key_cache, value_cache, block_tables,
+                                                  context_lens, num_kv_heads)
     if query_start.shape != (S + 1,):
         raise ValueError("query_start must be [S + 1]")
-    _one_device((out, q, key_cache, value_cache, block_tables, context_lens, query_start))
-    ws_ptr, ws_bytes = _workspace(workspace)
-    _check(pa_prefill_window(_dev(out, "out"), _dev(q, "q"), _dev(key_cache, "key_cache"),
-                             _dev(value_cache, "value_cache"),
-                             _dev(block_tables, "block_tables", torch.int32),
-                             _dev(context_lens, "context_lens", torch.int32),
-                             _dev(query_start, "query_start", torch.int32),
+    dev, st = _device_stream(stream)
+    i32, dtype = _torch().int32, q.dtype
+    ws_ptr, ws_bytes = _workspace(workspace, dev)
+    _check(pa_prefill_window(_ptr(out, "out", dtype, dev), _ptr(q, "q", dtype, dev),
+                             _ptr(key_cache, "key_cache", dtype, dev),
+                             _ptr(value_cache, "value_cache", dtype, dev),
+                             _ptr(block_tables, "block_tables", i32, dev),
+                             _ptr(context_lens, "context_lens", i32, dev),
+                             _ptr(query_start, "query_start", i32, dev),
                              _i32_arg(max_query_len, "max_query_len"), _i32_arg(window, "window"),
-                             _i32_arg(num_sinks, "num_sinks"), num_kv_heads, float(scale), S, hq,
-                             q.shape[0], d, bs, block_tables.shape[1], nb, dtype_code(q), ws_ptr,
-                             ws_bytes, _stream(stream)), "pa_prefill_window")
+                             _i32_arg(num_sinks, "num_sinks"), num_kv_heads, scale, S, hq, rows, d,
+                             bs, maxb, nb, dtype_code(q), ws_ptr, ws_bytes, st),
+           "pa_prefill_window")
 
 
 class Rope:
@@ -442,25 +453,24 @@ class Rope:
         if num_axes is None:
             num_axes = 1 if axes is None else int(axes.max()) + 1
         self._struct = RopeStruct()
-        _check(pa_rope_init(ctypes.byref(self._struct), freq.ctypes.data,
-                            None if axes is None else axes.ctypes.data, int(freq.size),
-                            int(num_axes), int(bool(interleaved))), "pa_rope_init")
         self._ref = ctypes.byref(self._struct)
+        _check(pa_rope_init(self._ref, freq.ctypes.data, None if axes is None else axes.ctypes.data,
+                            int(freq.size), int(num_axes), int(bool(interleaved))), "pa_rope_init")
         self.num_pairs = int(freq.size)
         self.num_axes = int(num_axes)
         self.interleaved = bool(interleaved)
 
 
-def _rows(t, name, heads, d, dtype):
-    """Pointer and token stride of [T][heads][d] whose heads lie contiguously."""
-    if t.dim() != 3 or t.shape[1] != heads or t.shape[2] != d or t.dtype != dtype:
-        raise ValueError(f"{name} must be [T, {heads}, {d}] {dtype}, got {tuple(t.shape)} {t.dtype}")
-    if not t.is_cuda:
-        raise ValueError(f"{name} must be a CUDA tensor")
-    st, sh, sd = t.stride()
-    if t.numel() and ((d > 1 and sd != 1) or (heads > 1 and sh != d)):
+def _rows(t, name, shape, dtype, dev):
+    """Address and token stride of a [T][heads][d] tensor whose heads lie contiguously."""
+    if t.shape != shape or t.dtype is not dtype or t.get_device() != dev:
+        raise ValueError(f"{name} must be {list(shape)} {dtype} on the current CUDA device, got "
+                         f"{list(t.shape)} {t.dtype} on {t.device}")
+    T, heads, d = shape
+    step, sh, sd = t.stride()
+    if (sd != 1 or (sh != d and heads > 1)) and T * heads > 0:
         raise ValueError(f"{name}: the heads of a token must be contiguous")
-    return ctypes.c_void_p(t.data_ptr()), st if t.shape[0] > 1 else 0
+    return t.data_ptr(), step if T > 1 else 0
 
 
 def rope_and_cache(q_out, q, k, v, key_cache, value_cache, slot_mapping, positions, rope: Rope,
@@ -472,24 +482,23 @@ def rope_and_cache(q_out, q, k, v, key_cache, value_cache, slot_mapping, positio
     (q itself if contiguous); positions int32 [rope.num_axes][T];
     slot_mapping int64 [T], negative for padding."""
     torch = _torch()
-    nb, hkv, bs, d = _cache_shape(key_cache, value_cache)
-    T = slot_mapping.shape[0]
-    hq = q.shape[1]
-    if q_out.shape != q.shape or q_out.dtype != q.dtype:
-        raise ValueError("q_out must be like q")
-    if q.shape[0] != T or k.shape[0] != T or v.shape[0] != T:
-        raise ValueError(f"q, k and v must have {T} tokens")
-    if tuple(positions.shape) != (rope.num_axes, T):
-        raise ValueError(f"positions must be [{rope.num_axes}, {T}]")
-    _one_device((q_out, q, k, v, key_cache, value_cache, slot_mapping, positions))
-    qp, qs = _rows(q, "q", hq, d, key_cache.dtype)
-    kp, ks = _rows(k, "k", hkv, d, key_cache.dtype)
-    vp, vs = _rows(v, "v", hkv, d, key_cache.dtype)
-    _check(pa_rope_and_cache(_dev(q_out, "q_out"), qp, kp, vp, _dev(key_cache, "key_cache"),
-                             _dev(value_cache, "value_cache"),
-                             _dev(slot_mapping, "slot_mapping", torch.int64, 1),
-                             _dev(positions, "positions", torch.int32, 2), rope._ref, qs, ks, vs, T,
-                             hq, hkv, d, bs, nb, dtype_code(key_cache), _stream(stream)),
+    nb, hkv, bs, d = key_cache.shape
+    if value_cache.shape != key_cache.shape:
+        raise ValueError("key_cache and value_cache must match")
+    T, hq, _ = q_out.shape
+    if slot_mapping.shape != (T,) or positions.shape != (rope.num_axes, T):
+        raise ValueError(f"slot_mapping must be [{T}], positions [{rope.num_axes}, {T}]")
+    dtype = key_cache.dtype
+    dev, st = _device_stream(stream)
+    qp, qs = _rows(q, "q", (T, hq, d), dtype, dev)
+    kp, ks = _rows(k, "k", (T, hkv, d), dtype, dev)
+    vp, vs = _rows(v, "v", (T, hkv, d), dtype, dev)
+    _check(pa_rope_and_cache(_ptr(q_out, "q_out", dtype, dev), qp, kp, vp,
+                             _ptr(key_cache, "key_cache", dtype, dev),
+                             _ptr(value_cache, "value_cache", dtype, dev),
+                             _ptr(slot_mapping, "slot_mapping", torch.int64, dev),
+                             _ptr(positions, "positions", torch.int32, dev), rope._ref, qs, ks, vs,
+                             T, hq, hkv, d, bs, nb, dtype_code(key_cache), st),
            "pa_rope_and_cache")
 
 

@@ -817,9 +817,9 @@ int launch_window_kernel(const WindowArgs &a, const CUtensorMap &tmk, const CUte
 template <typename T, int D, bool CHUNK>
 int launch_window_merge(const WindowArgs &a, cudaStream_t st) {
     const int64_t rows = (int64_t)a.d.num_seqs * a.max_query_len * a.d.num_q_heads;
-    return launch_pdl(merge_window_kernel<T, D, CHUNK>,
-                      dim3((unsigned)((rows + kMergeRows - 1) / kMergeRows)), dim3(kMergeRows * 32),
-                      0, st, a);
+    const int per_cta = a.d.num_parts > kMergeFew ? 1 : kMergeRows;
+    return launch_pdl(merge_window_kernel<T, D, CHUNK>, dim3((unsigned)((rows + per_cta - 1) / per_cta)),
+                      dim3(kMergeRows * 32), 0, st, a);
 }
 
 template <typename T, int D, bool CHUNK>
@@ -1036,7 +1036,7 @@ int pa_prefill_window(void *out, const void *q, const void *key_cache, const voi
         return PA_ERR_INVALID_ARG;
     max_query_len = std::min(max_query_len, num_q_tokens);
     if ((int64_t)num_seqs * num_kv_heads >= (int64_t(1) << 31) ||
-        (int64_t)num_seqs * max_query_len >= (int64_t(1) << 33) / num_q_heads)
+        (int64_t)num_seqs * max_query_len >= (int64_t(1) << 31) / num_q_heads)
         return PA_ERR_UNSUPPORTED;
     window = std::min(window, kWindowMax);
     num_sinks = std::min(num_sinks, kWindowMax);

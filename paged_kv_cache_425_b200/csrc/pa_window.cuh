@@ -344,16 +344,76 @@ __global__ void __launch_bounds__(NW * 32, NT == 1 ? PA_DECODE_MIN_CTAS : 3)
     }
 }
 
-// Joins the partitions of rows whose visible blocks were split: one warp per
-// row of q, as in merge_kernel.  Rows share their partitions with the other
-// tokens of their tile (all of the sequence's, in decode_window_kernel).
+// Joins the partitions of one row with the four warps of a CTA: warp w takes
+// every fourth partition and has eight of them in flight, and every warp works
+// out all the weights.  merge_row's single warp takes partition after
+// partition, about 10 us for the 65 of one 8192-token window.
+template <typename T, int D>
+__device__ __forceinline__ void merge_row_cta(const DecodeArgs &a, size_t row, int nparts) {
+    constexpr int D4 = D / 4, PER = 32 / kMergeRows;
+    __shared__ float4 s_acc[kMergeRows][D4];
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const float2 *ml = a.ws_ml + row * a.num_parts;
+    const float4 *op = reinterpret_cast<const float4 *>(a.ws_o + row * a.num_parts * D);
+    float4 x[PER], acc = make_float4(0.f, 0.f, 0.f, 0.f);
+    auto load = [&](int p0) {
+#pragma unroll
+        for (int j = 0; j < PER; ++j) {
+            const int p = p0 + warp + j * kMergeRows;
+            if (p < nparts && lane < D4) x[j] = op[(size_t)p * D4 + lane];
+        }
+    };
+    load(0);  // does not depend on the weights
+    float M = -INFINITY, den = 0.f;
+    for (int p = lane; p < nparts; p += 32) {
+        const float2 v = ml[p];
+        if (v.y > 0.f) M = fmaxf(M, v.x);
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
+    for (int p0 = 0; p0 < nparts; p0 += 32) {
+        if (p0 > 0) load(p0);
+        const float2 v = p0 + lane < nparts ? ml[p0 + lane] : make_float2(0.f, 0.f);
+        const float w = v.y > 0.f ? v.y * fast_exp2(v.x - M) : 0.f;
+        den += w;
+#pragma unroll
+        for (int j = 0; j < PER; ++j) {
+            const float wj = __shfl_sync(0xffffffffu, w, warp + j * kMergeRows);
+            if (p0 + warp + j * kMergeRows < nparts && lane < D4) {
+                acc.x += wj * x[j].x; acc.y += wj * x[j].y; acc.z += wj * x[j].z; acc.w += wj * x[j].w;
+            }
+        }
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) den += __shfl_xor_sync(0xffffffffu, den, o);
+    if (lane < D4) s_acc[warp][lane] = acc;
+    __syncthreads();
+    if (warp == 0 && lane < D4) {
+#pragma unroll
+        for (int w = 1; w < kMergeRows; ++w) {
+            const float4 y = s_acc[w][lane];
+            acc.x += y.x; acc.y += y.y; acc.z += y.z; acc.w += y.w;
+        }
+        const float inv = den > 0.f ? 1.f / den : 0.f;
+        uint16_t *out = reinterpret_cast<uint16_t *>(a.out) + row * D + 4 * lane;
+        const uint32_t lo = (uint32_t)narrow1(acc.x * inv, T()) | ((uint32_t)narrow1(acc.y * inv, T()) << 16);
+        const uint32_t hi = (uint32_t)narrow1(acc.z * inv, T()) | ((uint32_t)narrow1(acc.w * inv, T()) << 16);
+        *reinterpret_cast<uint2 *>(out) = make_uint2(lo, hi);
+    }
+}
+
+// Joins the partitions of rows whose visible blocks were split: a row of q per
+// warp, or per CTA when a row can have more than kMergeFew partitions.  Rows
+// share their partitions with the other tokens of their tile (all of the
+// sequence's, in decode_window_kernel).
 template <typename T, int D, bool CHUNK>
 __global__ void __launch_bounds__(kMergeRows * 32) merge_window_kernel(const WindowArgs wa) {
     const DecodeArgs &a = wa.d;
     pdl_launch_dependents();
     pdl_wait_prior();
     const int lane = threadIdx.x & 31;
-    const size_t id = (size_t)blockIdx.x * kMergeRows + (threadIdx.x >> 5);
+    const bool whole_cta = a.num_parts > kMergeFew;
+    const size_t id = whole_cta ? blockIdx.x : (size_t)blockIdx.x * kMergeRows + (threadIdx.x >> 5);
     const size_t per_seq = (size_t)wa.max_query_len * a.num_q_heads;
     const int s = (int)(id / per_seq);
     if (s >= a.num_seqs) return;
@@ -369,7 +429,10 @@ __global__ void __launch_bounds__(kMergeRows * 32) merge_window_kernel(const Win
     const int nparts = (w.nv + a.part_blocks - 1) / a.part_blocks;
     if (nparts <= 1) return;
     const size_t row = (size_t)(w.q0 + i) * a.num_q_heads + id % a.num_q_heads;
-    merge_row<T, D>(a, row, nparts, lane);
+    if (whole_cta)
+        merge_row_cta<T, D>(a, row, nparts);
+    else
+        merge_row<T, D>(a, row, nparts, lane);
 }
 
 }  // namespace pa
