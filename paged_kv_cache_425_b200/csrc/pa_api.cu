@@ -165,14 +165,14 @@ unsigned long long current_context_id() {
     return id;
 }
 
-// Raise a kernel's dynamic shared-memory limit to `bytes` (once per kernel,
-// device, CUDA context and size: the attribute persists in the context, and a
+// Set an attribute of a kernel to at least `value` (once per kernel,
+// attribute, device, CUDA context and value: it persists in the context, and a
 // device reset starts a new one).
 template <typename Kernel>
-bool set_smem(Kernel k, int bytes) {
+bool set_attribute(Kernel k, cudaFuncAttribute attr, int value) {
     struct Key {
         const void *fn;
-        int dev, bytes;
+        int attr, dev, value;
         unsigned long long ctx;
     };
     static std::mutex mu;
@@ -183,11 +183,24 @@ bool set_smem(Kernel k, int bytes) {
     const void *fn = reinterpret_cast<const void *>(k);
     std::lock_guard<std::mutex> lock(mu);
     for (const Key &e : done)
-        if (ctx != 0 && e.fn == fn && e.dev == dev && e.ctx == ctx && e.bytes >= bytes) return true;
-    if (cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes) != cudaSuccess)
-        return false;
-    if (ctx != 0) done.push_back({fn, dev, bytes, ctx});
+        if (ctx != 0 && e.fn == fn && e.attr == attr && e.dev == dev && e.ctx == ctx &&
+            e.value >= value)
+            return true;
+    if (cudaFuncSetAttribute(k, attr, value) != cudaSuccess) return false;
+    if (ctx != 0) done.push_back({fn, attr, dev, value, ctx});
     return true;
+}
+
+// Raise a kernel's dynamic shared-memory limit to `bytes`.
+template <typename Kernel>
+bool set_smem(Kernel k, int bytes) {
+    return set_attribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+}
+
+// Allow clusters of more than 8 CTAs.
+template <typename Kernel>
+bool allow_cluster16(Kernel k) {
+    return set_attribute(k, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
 }
 
 // Registers per thread a kernel was compiled with (-1 on failure); looked up
@@ -332,7 +345,8 @@ int launch_prefill_umma(void *out, const void *q, const void *key_cache, const v
                         const int32_t *query_start, int32_t max_query_len, int32_t num_kv_heads,
                         float scale, int32_t num_seqs, int32_t num_q_heads, int32_t num_q_tokens,
                         int32_t head_dim, int32_t max_blocks_per_seq, int64_t num_blocks,
-                        int32_t dtype, const PrefillWindow *pw, cudaStream_t st) {
+                        int32_t dtype, const PrefillWindow *pw, cudaStream_t st,
+                        PrefillArgs *used = nullptr) {
     const int group = num_q_heads / num_kv_heads;
     const int tokens_per_tile = kUmmaRows / group;
     const int64_t rows_per_cta = (int64_t)kUmmaQTiles * tokens_per_tile * group;
@@ -351,6 +365,7 @@ int launch_prefill_umma(void *out, const void *q, const void *key_cache, const v
     a.num_q_tokens = num_q_tokens;
     a.scale_log2 = scale * 1.4426950408889634f;
     a.tiles_per_seq = (int)tiles;
+    if (used) *used = a;
     CUtensorMap tmq, tmk, tmv;
     if (!encode_q_map(&tmq, q, num_q_tokens, num_q_heads, num_kv_heads, head_dim, dtype,
                       tokens_per_tile) ||
@@ -766,52 +781,122 @@ int64_t window_visible_blocks(int32_t max_blocks_per_seq, int32_t queries, int32
     return std::min<int64_t>(max_blocks_per_seq, w + k);
 }
 
-// Blocks per partition of a windowed decode (see decode_window_kernel):
-// PA_PARTITION_TOKENS, but shorter while the grid would leave resident CTA
-// slots of the GPU (148 SMs x 6 CTAs) empty.
-constexpr int kWindowFill = 148 * PA_DECODE_MIN_CTAS;
-int window_part_blocks(int64_t seq_heads, int64_t visible) {
-    int pb = kPartBlocks;
-    while (pb > 8 && seq_heads * ((visible + pb - 1) / pb) < kWindowFill) pb /= 2;
-    return pb;
-}
-
-// Rows of a kv head (query tokens x group) up to which a chunk runs on
-// decode_window_kernel.
-constexpr int kChunkRows = 16;
-
-struct PrefillSplit {
-    int splits, split_tiles;
+// How a windowed call runs: on decode_window_kernel (runs of tile_tokens query
+// tokens; few rows: `cluster` CTAs each, many: `parts` partitions each), or on
+// prefill_umma_kernel (umma; `parts` ranges of split_tiles key tiles).
+struct WindowPlan {
+    bool umma;
+    int tile_tokens, cluster, part_blocks, split_tiles;
+    int64_t parts;
+    // rows of the workspace, each with `parts` partial results
+    int64_t ws_rows;
 };
 
-// Key-tile ranges per work item of a windowed prefill.
-PrefillSplit prefill_split(int32_t num_seqs, int32_t max_query_len, int32_t num_q_heads,
-                           int32_t num_kv_heads, int32_t max_blocks_per_seq, int32_t window,
-                           int32_t num_sinks) {
-    constexpr int kSms = 148, kMinTiles = 2;
+constexpr int kWindowSms = 148;
+constexpr int kChunkRows = 16;  // rows of a run on decode_window_kernel
+// Shapes of decode_window_kernel (see there): warps and, for the two with few
+// CTAs per SM, blocks in flight per warp.  A lane holds one block id, so a CTA
+// takes 32 blocks per warp at most.
+constexpr int kFewWarps = 8, kManyWarps = 4, kWindowStages = 3;
+constexpr int kFewBlocks = 32 * kFewWarps, kManyBlocks = 32 * kManyWarps;
+
+WindowPlan window_plan(int64_t num_seqs, int32_t num_q_tokens, int32_t max_query_len, int32_t num_q_heads,
+                       int32_t num_kv_heads, int32_t max_blocks_per_seq, int32_t window,
+                       int32_t num_sinks) {
     const int group = num_q_heads / num_kv_heads;
-    const int tile_tokens = kUmmaQTiles * (kUmmaRows / group);
-    const int64_t items = (int64_t)num_seqs * num_kv_heads *
-                          ((max_query_len + tile_tokens - 1) / tile_tokens);
-    const int64_t blocks = window_visible_blocks(
-        max_blocks_per_seq, std::min(max_query_len, tile_tokens), window, num_sinks);
-    const int64_t tiles = (blocks + 7) / 8;
-    int64_t splits = std::min<int64_t>(std::max<int64_t>(kSms / items, 1), (tiles + kMinTiles - 1) / kMinTiles);
-    PrefillSplit r;
-    r.split_tiles = (int)((tiles + splits - 1) / splits);
-    r.splits = (int)((tiles + r.split_tiles - 1) / r.split_tiles);
-    return r;
+    WindowPlan p = {};
+    p.ws_rows = (int64_t)num_q_tokens * num_q_heads;
+    // decode_window_kernel: runs of at most kChunkRows rows
+    const int64_t run_tokens =
+        max_query_len * (int64_t)group <= 8 ? max_query_len : std::max(kChunkRows / group, 1);
+    const int64_t runs = num_seqs * num_kv_heads * ((max_query_len + run_tokens - 1) / run_tokens);
+    const int64_t blocks =
+        window_visible_blocks(max_blocks_per_seq, (int32_t)run_tokens, window, num_sinks);
+    // prefill_umma_kernel: items of two query tiles, walked in tiles of 128 keys
+    constexpr int kTileBlocks = kUmmaKeys / kBlock;
+    const int64_t item_tokens = kUmmaQTiles * (kUmmaRows / group);
+    const int64_t items = num_seqs * num_kv_heads * ((max_query_len + item_tokens - 1) / item_tokens);
+    const int64_t tiles =
+        (window_visible_blocks(max_blocks_per_seq, (int32_t)std::min<int64_t>(max_query_len, item_tokens),
+                               window, num_sinks) + kTileBlocks - 1) / kTileBlocks;
+    // Few rows keep most of a 256-row item empty.  The decode kernel takes about
+    // 1.5 ns per (run, block) while one wave holds the runs, the other about
+    // 2.4 us per key tile on each of the 148 SMs and 5 us more at its ends; 90
+    // measured shapes choose by that within 20 % of the better one (40 tokens,
+    // window 100: 6.5 us here, 10.3 us there; 32 tokens of 4 heads, window 4096:
+    // 29 us here, 24 us there).
+    p.umma = group > kChunkRows ||
+             (max_query_len > 1 && (int64_t)max_query_len * group > 8 &&
+              (runs > 2 * kWindowSms || runs * blocks > 3500 + 11 * items * tiles));
+    if (p.umma) {
+        p.tile_tokens = (int)item_tokens;
+        // Key ranges per item, each at least two tiles: the fewest microseconds
+        // over the rounds that 148 CTAs need (2.1 per tile, 2.5 per item), plus
+        // the launch and the traffic of joining them.
+        double best = 0;
+        for (int64_t n = 1; n <= 64 && (n == 1 || 2 * n <= tiles + 1); ++n) {
+            const int64_t per = (tiles + n - 1) / n, used = (tiles + per - 1) / per;
+            const double cost = (double)((items * used + kWindowSms - 1) / kWindowSms) * (2.1 * per + 2.5) +
+                                (used > 1 ? 3.0 + 0.04 * items * used : 0.0);
+            if (n == 1 || cost < best) {
+                best = cost;
+                p.parts = used;
+                p.split_tiles = (int)per;
+            }
+        }
+        p.ws_rows = items * kUmmaQTiles * kUmmaRows;
+        return p;
+    }
+    p.tile_tokens = (int)run_tokens;
+    p.parts = 1;
+    if (runs <= kWindowSms && blocks > kManyWarps) {
+        // A cluster as large as finds room for every run at once (at one CTA
+        // per SM the GPU holds 74, 33, 15 and 7 clusters of 2, 4, 8 and 16; a
+        // second wave doubles the time), while each warp keeps a block.
+        constexpr int kRoom[] = {74, 33, 15, 7};
+        int ctas = 1;
+        for (int i = 0; i < 4 && runs <= kRoom[i] && (blocks + ctas - 1) / ctas > kFewWarps; ++i)
+            ctas *= 2;
+        if ((blocks + ctas - 1) / ctas <= kFewBlocks) {
+            p.cluster = ctas;
+            return p;
+        }
+    }
+    if (runs <= 2 * kWindowSms && blocks > kManyWarps && blocks <= kManyBlocks) {
+        p.part_blocks = 0;  // one CTA per run, all at once (256 runs of 64 blocks: 24.3 us, split 28.5)
+        return p;
+    }
+    // 512-token partitions, or 1024 where that still makes several of a run
+    // (1024 runs of 258 blocks: 314 us, 325 with the shorter ones; 384 runs of
+    // up to 131: 63.3 and 61.7)
+    p.part_blocks = blocks >= 8 * kPartBlocks ? 2 * kPartBlocks : kPartBlocks;
+    p.parts = (blocks + p.part_blocks - 1) / p.part_blocks;
+    return p;
 }
 
-template <typename T, int D, int NT, int PB, bool CHUNK>
+template <typename T, int D, int NW, int ST, int U, int PB, int NT, bool CHUNK, bool CLUSTER>
 int launch_window_kernel(const WindowArgs &a, const CUtensorMap &tmk, const CUtensorMap &tmv,
                          cudaStream_t st) {
-    constexpr int STAGES = D == 128 ? kStages128 : kStages64;
-    constexpr int SMEM = kWarps * STAGES * WarpPipe<D, STAGES>::kStage + 1024;
-    const dim3 grid(a.d.num_seqs * a.d.num_kv_heads, a.d.num_parts);
-    auto k = decode_window_kernel<T, D, kWarps, STAGES, NT, PB, CHUNK>;
-    if (!set_smem(k, SMEM)) return PA_ERR_CUDA;
-    return launch_pdl(k, grid, dim3(kWarps * 32), SMEM, st, tmk, tmv, a);
+    constexpr int STAGES = (D == 128 ? 1 : 2) * ST;  // the same bytes in flight
+    constexpr int SMEM = NW * STAGES * WarpPipe<D, STAGES>::kStage + 1024;
+    auto k = decode_window_kernel<T, D, NW, STAGES, U, PB, NT, CHUNK, CLUSTER>;
+    if (!set_smem(k, SMEM) || (CLUSTER && !allow_cluster16(k))) return PA_ERR_CUDA;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(a.d.num_seqs * a.d.num_kv_heads, CLUSTER ? a.cluster : a.d.num_parts,
+                       (a.max_query_len + a.tile_tokens - 1) / a.tile_tokens);
+    cfg.blockDim = dim3(NW * 32);
+    cfg.dynamicSmemBytes = SMEM;
+    cfg.stream = st;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = 1;
+    attr[1].val.clusterDim.y = CLUSTER ? a.cluster : 1;
+    attr[1].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = CLUSTER ? 2 : 1;
+    return cudaLaunchKernelEx(&cfg, k, tmk, tmv, a) == cudaSuccess ? PA_OK : PA_ERR_CUDA;
 }
 
 template <typename T, int D, bool CHUNK>
@@ -825,33 +910,36 @@ int launch_window_merge(const WindowArgs &a, cudaStream_t st) {
 template <typename T, int D, bool CHUNK>
 int launch_window(const WindowArgs &a, const CUtensorMap &tmk, const CUtensorMap &tmv,
                   cudaStream_t st) {
-    const int rows = a.max_query_len * (a.d.num_q_heads / a.d.num_kv_heads);
-    auto with_pb = [&](auto nt) -> int {
+    const int rows = a.tile_tokens * (a.d.num_q_heads / a.d.num_kv_heads);
+    auto with_rows = [&](auto nt) -> int {
         constexpr int NT = decltype(nt)::value;
-        switch (a.d.part_blocks) {
-            case 8: return launch_window_kernel<T, D, NT, 8, CHUNK>(a, tmk, tmv, st);
-            case 16: return launch_window_kernel<T, D, NT, 16, CHUNK>(a, tmk, tmv, st);
-            default: return launch_window_kernel<T, D, NT, kPartBlocks, CHUNK>(a, tmk, tmv, st);
-        }
+        if (a.cluster > 1)
+            return launch_window_kernel<T, D, kFewWarps, kWindowStages, 2, 0, NT, CHUNK, true>(a, tmk, tmv, st);
+        if (a.cluster == 1)
+            return launch_window_kernel<T, D, kFewWarps, kWindowStages, 2, 0, NT, CHUNK, false>(a, tmk, tmv, st);
+        if (a.d.part_blocks == kPartBlocks)
+            return launch_window_kernel<T, D, kManyWarps, 1, 1, kPartBlocks, NT, CHUNK, false>(a, tmk, tmv, st);
+        if (a.d.part_blocks == 2 * kPartBlocks)
+            return launch_window_kernel<T, D, kManyWarps, 1, 1, 2 * kPartBlocks, NT, CHUNK, false>(a, tmk, tmv, st);
+        return launch_window_kernel<T, D, kManyWarps, kWindowStages, 2, 0, NT, CHUNK, false>(a, tmk, tmv, st);
     };
-    const int rc = rows <= 8 ? with_pb(std::integral_constant<int, 1>{})
-                             : with_pb(std::integral_constant<int, 2>{});
+    const int rc = rows <= 8 ? with_rows(std::integral_constant<int, 1>{})
+                             : with_rows(std::integral_constant<int, 2>{});
     if (rc != PA_OK || a.d.num_parts <= 1) return rc;
     return launch_window_merge<T, D, CHUNK>(a, st);
 }
 
-// Workspace of a windowed call: `rows` query rows (token x head), `parts`
-// partitions each; nothing when no row can be split.
-size_t window_workspace(int64_t rows, int64_t head_dim, int64_t parts) {
-    return parts <= 1 ? 0 : (size_t)workspace_layout(1, rows, head_dim, parts).total;
+size_t window_workspace(const WindowPlan &p, int64_t head_dim) {
+    return p.parts <= 1 ? 0 : (size_t)workspace_layout(1, p.ws_rows, head_dim, p.parts).total;
 }
 
-int take_workspace(DecodeArgs &a, int64_t rows, int64_t head_dim, void *workspace,
+int take_workspace(DecodeArgs &a, const WindowPlan &p, int64_t head_dim, void *workspace,
                    size_t workspace_bytes) {
     a.ws_o = nullptr;
     a.ws_ml = nullptr;
-    if (a.num_parts <= 1) return PA_OK;
-    const WorkspaceLayout l = workspace_layout(1, rows, head_dim, a.num_parts);
+    a.num_parts = (int)p.parts;
+    if (p.parts <= 1) return PA_OK;
+    const WorkspaceLayout l = workspace_layout(1, p.ws_rows, head_dim, p.parts);
     if (!workspace || workspace_bytes < (size_t)l.total || !aligned(workspace, 256))
         return PA_ERR_WORKSPACE;
     char *base = static_cast<char *>(workspace);
@@ -902,7 +990,8 @@ int decode_window_call(void *out, const void *q, const void *k_new, const void *
         return PA_ERR_INVALID_ARG;
     window = std::min(window, kWindowMax);
     num_sinks = std::min(num_sinks, kWindowMax);
-    const int64_t visible = window_visible_blocks(max_blocks_per_seq, 1, window, num_sinks);
+    const WindowPlan plan = window_plan(num_seqs, num_seqs, 1, num_q_heads, num_kv_heads, max_blocks_per_seq,
+                                        window, num_sinks);
     WindowArgs a = {};
     a.d.out = out;
     a.d.q = q;
@@ -913,10 +1002,9 @@ int decode_window_call(void *out, const void *q, const void *k_new, const void *
     a.d.num_q_heads = num_q_heads;
     a.d.num_kv_heads = num_kv_heads;
     a.d.max_blocks_per_seq = max_blocks_per_seq;
-    a.d.part_blocks = window_part_blocks((int64_t)num_seqs * num_kv_heads, visible);
-    const int64_t parts = (visible + a.d.part_blocks - 1) / a.d.part_blocks;
-    if (parts > 65535) return PA_ERR_UNSUPPORTED;
-    a.d.num_parts = (int)parts;
+    if (plan.parts > 65535) return PA_ERR_UNSUPPORTED;
+    a.cluster = plan.cluster;
+    a.d.part_blocks = plan.part_blocks;
     a.d.scale_log2 = scale * 1.4426950408889634f;
     a.d.k_new = append ? k_new : nullptr;
     a.d.v_new = append ? v_new : nullptr;
@@ -926,28 +1014,10 @@ int decode_window_call(void *out, const void *q, const void *k_new, const void *
     a.tile_tokens = 1;
     a.window = window;
     a.num_sinks = num_sinks;
-    rc = take_workspace(a.d, (int64_t)num_seqs * num_q_heads, head_dim, workspace, workspace_bytes);
+    rc = take_workspace(a.d, plan, head_dim, workspace, workspace_bytes);
     if (rc != PA_OK) return rc;
     return window_call<false>(a, head_dim, dtype, key_cache, value_cache,
                               static_cast<cudaStream_t>(stream));
-}
-
-// Partitions (decode_window_kernel) or splits (prefill_umma_kernel) per row.
-int64_t prefill_window_parts(int32_t num_seqs, int32_t max_query_len, int32_t num_q_heads,
-                             int32_t num_kv_heads, int32_t max_blocks_per_seq, int32_t window,
-                             int32_t num_sinks, bool *rows_fit, int *part_blocks) {
-    const int group = num_q_heads / num_kv_heads;
-    *rows_fit = (int64_t)max_query_len * group <= kChunkRows;
-    if (*rows_fit) {
-        const int64_t visible =
-            window_visible_blocks(max_blocks_per_seq, max_query_len, window, num_sinks);
-        *part_blocks = window_part_blocks((int64_t)num_seqs * num_kv_heads, visible);
-        return (visible + *part_blocks - 1) / *part_blocks;
-    }
-    const PrefillSplit sp = prefill_split(num_seqs, max_query_len, num_q_heads, num_kv_heads,
-                                          max_blocks_per_seq, window, num_sinks);
-    *part_blocks = sp.split_tiles * (kUmmaKeys / kBlock);
-    return sp.splits;
 }
 
 }  // namespace
@@ -962,9 +1032,9 @@ size_t pa_decode_window_workspace_size(int32_t num_seqs, int32_t num_q_heads, in
     if (num_seqs <= 0 || num_q_heads <= 0 || num_kv_heads <= 0 || head_dim <= 0 ||
         block_size != kBlock || max_blocks_per_seq <= 0 || window < 1 || num_sinks < 0)
         return 0;
-    const int64_t visible = window_visible_blocks(max_blocks_per_seq, 1, window, num_sinks);
-    const int pb = window_part_blocks((int64_t)num_seqs * num_kv_heads, visible);
-    return window_workspace((int64_t)num_seqs * num_q_heads, head_dim, (visible + pb - 1) / pb);
+    return window_workspace(window_plan(num_seqs, num_seqs, 1, num_q_heads, num_kv_heads,
+                                        max_blocks_per_seq, window, num_sinks),
+                            head_dim);
 }
 
 int pa_decode_window(void *out, const void *q, const void *key_cache, const void *value_cache,
@@ -1003,11 +1073,9 @@ size_t pa_prefill_window_workspace_size(int32_t num_seqs, int32_t num_q_tokens,
         block_size != kBlock || max_blocks_per_seq <= 0 || window < 1 || num_sinks < 0)
         return 0;
     max_query_len = std::min(max_query_len, num_q_tokens);
-    bool rows_fit;
-    int pb;
-    const int64_t parts = prefill_window_parts(num_seqs, max_query_len, num_q_heads, num_kv_heads,
-                                               max_blocks_per_seq, window, num_sinks, &rows_fit, &pb);
-    return window_workspace((int64_t)num_q_tokens * num_q_heads, head_dim, parts);
+    return window_workspace(window_plan(num_seqs, num_q_tokens, max_query_len, num_q_heads,
+                                        num_kv_heads, max_blocks_per_seq, window, num_sinks),
+                            head_dim);
 }
 
 int pa_prefill_window(void *out, const void *q, const void *key_cache, const void *value_cache,
@@ -1041,12 +1109,12 @@ int pa_prefill_window(void *out, const void *q, const void *key_cache, const voi
     window = std::min(window, kWindowMax);
     num_sinks = std::min(num_sinks, kWindowMax);
 
-    bool rows_fit;
+    const WindowPlan plan = window_plan(num_seqs, num_q_tokens, max_query_len, num_q_heads, num_kv_heads,
+                                        max_blocks_per_seq, window, num_sinks);
+    if (plan.parts > 65535) return PA_ERR_UNSUPPORTED;
     WindowArgs a = {};
-    const int64_t parts = prefill_window_parts(num_seqs, max_query_len, num_q_heads, num_kv_heads,
-                                               max_blocks_per_seq, window, num_sinks, &rows_fit,
-                                               &a.d.part_blocks);
-    if (parts > 65535) return PA_ERR_UNSUPPORTED;
+    a.cluster = plan.cluster;
+    a.d.part_blocks = plan.part_blocks;
     a.d.out = out;
     a.d.q = q;
     a.d.block_tables = block_tables;
@@ -1056,38 +1124,39 @@ int pa_prefill_window(void *out, const void *q, const void *key_cache, const voi
     a.d.num_q_heads = num_q_heads;
     a.d.num_kv_heads = num_kv_heads;
     a.d.max_blocks_per_seq = max_blocks_per_seq;
-    a.d.num_parts = (int)parts;
     a.d.scale_log2 = scale * 1.4426950408889634f;
     a.query_start = query_start;
     a.num_q_tokens = num_q_tokens;
     a.max_query_len = max_query_len;
-    a.tile_tokens = rows_fit ? max_query_len : kUmmaQTiles * (kUmmaRows / group);
+    a.tile_tokens = plan.tile_tokens;
     a.window = window;
     a.num_sinks = num_sinks;
-    rc = take_workspace(a.d, (int64_t)num_q_tokens * num_q_heads, head_dim, workspace,
-                        workspace_bytes);
+    rc = take_workspace(a.d, plan, head_dim, workspace, workspace_bytes);
     if (rc != PA_OK) return rc;
     cudaStream_t st = static_cast<cudaStream_t>(stream);
-    if (rows_fit) return window_call<true>(a, head_dim, dtype, key_cache, value_cache, st);
+    if (!plan.umma) return window_call<true>(a, head_dim, dtype, key_cache, value_cache, st);
 
     PrefillWindow pw;
     pw.window = window;
     pw.num_sinks = num_sinks;
     pw.max_query_len = max_query_len;
-    pw.splits = (int)parts;
-    pw.split_tiles = a.d.part_blocks / (kUmmaKeys / kBlock);
-    pw.ws_o = a.d.ws_o;
+    pw.splits = (int)plan.parts;
+    pw.split_tiles = plan.split_tiles;
+    pw.ws_o = reinterpret_cast<float4 *>(a.d.ws_o);
     pw.ws_ml = a.d.ws_ml;
+    PrefillArgs pa;
     rc = launch_prefill_umma(out, q, key_cache, value_cache, block_tables, context_lens,
                              query_start, max_query_len, num_kv_heads, scale, num_seqs,
                              num_q_heads, num_q_tokens, head_dim, max_blocks_per_seq, num_blocks,
-                             dtype, &pw, st);
-    if (rc != PA_OK || parts <= 1) return rc;
+                             dtype, &pw, st, &pa);
+    if (rc != PA_OK || plan.parts <= 1) return rc;
+    const dim3 grid((unsigned)(plan.ws_rows / (kUmmaQTiles * kUmmaRows)),
+                    kUmmaQTiles * head_dim / (4 * kMergeVecs));
+    auto merge = [&](auto kernel) { return launch_pdl(kernel, grid, dim3(kUmmaRows), 0, st, pa, pw, a); };
     if (dtype == PA_F16)
-        return head_dim == 128 ? launch_window_merge<__half, 128, true>(a, st)
-                               : launch_window_merge<__half, 64, true>(a, st);
-    return head_dim == 128 ? launch_window_merge<__nv_bfloat16, 128, true>(a, st)
-                           : launch_window_merge<__nv_bfloat16, 64, true>(a, st);
+        return head_dim == 128 ? merge(merge_umma_kernel<__half, 128>) : merge(merge_umma_kernel<__half, 64>);
+    return head_dim == 128 ? merge(merge_umma_kernel<__nv_bfloat16, 128>)
+                           : merge(merge_umma_kernel<__nv_bfloat16, 64>);
 }
 
 // ---------------------------------------------------------------- rotary positions

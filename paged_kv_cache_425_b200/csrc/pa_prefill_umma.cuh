@@ -45,8 +45,8 @@
 // sees instead of the whole context: the sink blocks, then the window's,
 // packed into key tiles without a gap (a tile is gathered block by block
 // anyway), and mask each row to its own window.  With few items the tiles of
-// an item are split over several CTAs (w.splits); each writes its normalised
-// O, max and sum to the workspace and merge_window_kernel joins them.
+// an item are split over several CTAs (pw.splits); each writes its O, max and
+// sum to the workspace and merge_umma_kernel joins them.
 //
 // Warp 11 only completes the third warpgroup (setmaxnreg works per
 // warpgroup).  Every wait is bounded; a wait that gives up raises the CTA's abort flag, the
@@ -107,6 +107,11 @@ __device__ __forceinline__ float fmax3(float a, float b, float c) {
     return d;
 }
 
+// The lowest n bits set (all for n >= 32, none for n <= 0).
+__device__ __forceinline__ uint32_t bits_below(int n) {
+    return n >= 32 ? 0xffffffffu : n <= 0 ? 0u : (1u << n) - 1u;
+}
+
 // Wait for phase `parity` of `bar`; give up when the CTA's abort flag is
 // raised, or after kWaitTimeoutNs (then raise it and flag PA_DEVERR_TIMEOUT).
 __device__ __forceinline__ bool wait_or_abort(uint64_t *bar, uint32_t parity,
@@ -140,16 +145,24 @@ struct UmmaItem {
 struct PrefillWindow {
     int window, num_sinks, max_query_len;
     int splits, split_tiles;  // key-tile ranges per item, tiles in each
-    float *ws_o;              // [num_q_tokens][Hq][splits][D]
-    float2 *ws_ml;            // [num_q_tokens][Hq][splits]
+    // with more than one split: [item][splits][query tile][D / 4][128 rows] of
+    // four elements each, and (max, sum) [item][splits][query tile][128]; rows
+    // innermost, since a thread holds one row
+    float4 *ws_o;
+    float2 *ws_ml;
 };
+
+// Item's number in the workspace.
+__device__ __forceinline__ size_t umma_item_index(const PrefillArgs &a, int s, int tile, int kvh) {
+    return ((size_t)s * a.tiles_per_seq + tile) * a.num_kv_heads + kvh;
+}
 
 // Item i; false when it has no rows (a sequence with fewer query tokens than
 // the grid was sized for) or invalid bounds (reported by `report`).
 template <bool WIN>
 __device__ __forceinline__ bool umma_item(const PrefillArgs &a, const PrefillWindow &pw,
                                           const int *s_order, int i, int G, int rows_used,
-                                          bool report, UmmaItem &it) {
+                                          bool ranked, bool report, UmmaItem &it) {
     if constexpr (WIN) {
         it.part = i % pw.splits;
         i /= pw.splits;
@@ -158,7 +171,7 @@ __device__ __forceinline__ bool umma_item(const PrefillArgs &a, const PrefillWin
     const int rank = i / per_seq, rem = i % per_seq;
     it.tile = a.tiles_per_seq - 1 - rem / a.num_kv_heads;
     it.kvh = rem % a.num_kv_heads;
-    it.s = a.num_seqs <= kRankMax ? s_order[rank] : rank;
+    it.s = (WIN ? ranked : a.num_seqs <= kRankMax) ? s_order[rank] : rank;
     it.q0 = a.query_start[it.s];
     int n = a.query_start[it.s + 1] - it.q0;
     int L = a.context_lens[it.s];
@@ -250,7 +263,9 @@ __global__ void __launch_bounds__(kUmmaThreads, 1)
         fence_mbar_init();
         s_abort = 0;
     }
-    if (a.num_seqs <= kRankMax) {  // rank of each sequence by context length, ties by index
+    // (with one item per CTA the order does not matter)
+    const bool ranked = a.num_seqs <= kRankMax && !(WIN && total <= (int)gridDim.x);
+    if (ranked) {  // rank of each sequence by context length, ties by index
         int *s_len = reinterpret_cast<int *>(sk);  // the K ring is not in use yet
         for (int i = tid; i < a.num_seqs; i += kUmmaThreads) s_len[i] = a.context_lens[i];
         __syncthreads();
@@ -297,7 +312,7 @@ __global__ void __launch_bounds__(kUmmaThreads, 1)
             const int i = umma_round_item(r);
             if (i >= total) break;
             UmmaItem it;
-            if (!umma_item<WIN>(a, pw, s_order, i, G, rows_used, is_k && lane == 0, it)) continue;
+            if (!umma_item<WIN>(a, pw, s_order, i, G, rows_used, ranked, is_k && lane == 0, it)) continue;
             if (is_k) {
                 bool freed = true;
                 if (lane == 0) {
@@ -387,7 +402,7 @@ __global__ void __launch_bounds__(kUmmaThreads, 1)
                 const int i = umma_round_item(r);
                 if (i >= total) break;
                 UmmaItem it;
-                if (!umma_item<WIN>(a, pw, s_order, i, G, rows_used, false, it)) continue;
+                if (!umma_item<WIN>(a, pw, s_order, i, G, rows_used, ranked, false, it)) continue;
                 if (!(ok = wait_or_abort(q_full, items & 1, abort_flag) &&
                            wait_or_abort(&k_full[gt & 1], (gt >> 1) & 1, abort_flag)))
                     break;
@@ -452,7 +467,7 @@ __global__ void __launch_bounds__(kUmmaThreads, 1)
             const int i = umma_round_item(rr);
             if (i >= total) break;
             UmmaItem it;
-            if (!umma_item<WIN>(a, pw, s_order, i, G, rows_used, false, it)) continue;
+            if (!umma_item<WIN>(a, pw, s_order, i, G, rows_used, ranked, false, it)) continue;
             const int R = it.row0 + k * rows_used + r;
             const bool rvalid = r < rows_used && R < it.rows_total;
             const int qi = rvalid ? R / G : 0, qh = rvalid ? R % G : 0;
@@ -504,10 +519,17 @@ __global__ void __launch_bounds__(kUmmaThreads, 1)
                 if constexpr (WIN) {
                     // -infinity: a row may see nothing of its first tiles
                     if (vis_b > vis_a || vis_end < kUmmaKeys || bad) {
+                        // as four words of bits: comparisons per column take
+                        // four times as long as a whole unmasked tile
 #pragma unroll
-                        for (int c = 0; c < kUmmaKeys; ++c) {
-                            const bool seen = c < vis_a || (c >= vis_b && c < vis_end);
-                            if (!seen || ((bad >> (c >> 4)) & 1u)) x[c] = __float_as_uint(-INFINITY);
+                        for (int q = 0; q < 4; ++q) {
+                            uint32_t seen = bits_below(vis_a - 32 * q) |
+                                            (bits_below(vis_end - 32 * q) & ~bits_below(vis_b - 32 * q));
+                            if (bad & (1u << (2 * q))) seen &= 0xffff0000u;
+                            if (bad & (2u << (2 * q))) seen &= 0x0000ffffu;
+#pragma unroll
+                            for (int c = 0; c < 32; ++c)
+                                x[32 * q + c] = seen & (1u << c) ? x[32 * q + c] : __float_as_uint(-INFINITY);
                         }
                     }
                 } else if (key0 + kUmmaKeys - 1 > pos || bad) {
@@ -615,8 +637,9 @@ __global__ void __launch_bounds__(kUmmaThreads, 1)
             const float inv = l > 0.f ? 1.f / l : 0.f;
             if constexpr (WIN) {
                 if (it.nparts > 1) {  // one of several splits: its share to the workspace
-                    const size_t row = (size_t)(it.q0 + qi) * a.num_q_heads + (size_t)it.kvh * G + qh;
-                    float *wo = pw.ws_o + (row * pw.splits + it.part) * D;
+                    const size_t slot = ((umma_item_index(a, it.s, it.tile, it.kvh) * pw.splits + it.part) *
+                                             kUmmaQTiles + k) * kUmmaRows + r;
+                    float4 *wo = pw.ws_o + (slot - r) * (D / 4) + r;
 #pragma unroll
                     for (int c0 = 0; c0 < D; c0 += 32) {
                         uint32_t o[32];
@@ -624,14 +647,12 @@ __global__ void __launch_bounds__(kUmmaThreads, 1)
                         if (rvalid) {
 #pragma unroll
                             for (int u = 0; u < 8; ++u)
-                                *reinterpret_cast<float4 *>(wo + c0 + 4 * u) =
-                                    make_float4(__uint_as_float(o[4 * u]) * inv,
-                                                __uint_as_float(o[4 * u + 1]) * inv,
-                                                __uint_as_float(o[4 * u + 2]) * inv,
-                                                __uint_as_float(o[4 * u + 3]) * inv);
+                                wo[(c0 / 4 + u) * kUmmaRows] =
+                                    make_float4(__uint_as_float(o[4 * u]), __uint_as_float(o[4 * u + 1]),
+                                                __uint_as_float(o[4 * u + 2]), __uint_as_float(o[4 * u + 3]));
                         }
                     }
-                    if (rvalid) pw.ws_ml[row * pw.splits + it.part] = make_float2(m_run, l);
+                    if (rvalid) pw.ws_ml[slot] = make_float2(m_run, l);
                     tc_fence_before();
                     gt += it.ntiles;
                     ++items;
@@ -679,6 +700,73 @@ __global__ void __launch_bounds__(kUmmaThreads, 1)
         }
         tc_fence_before();
         __syncthreads();  // pairs with the teardown barrier of the other warpgroup
+    }
+}
+
+// Joins the splits of pa_prefill_window's items: block x = item, y = query tile
+// and 4 * kMergeVecs columns; thread r = row r of the tile.  Four splits are
+// in flight per thread.
+constexpr int kMergeVecs = 4;
+
+template <typename T, int D>
+__global__ void __launch_bounds__(kUmmaRows)
+    merge_umma_kernel(const PrefillArgs a, const PrefillWindow pw, const WindowArgs wa) {
+    constexpr int V = kMergeVecs, P = 4;
+    pdl_launch_dependents();
+    pdl_wait_prior();
+    const int r = threadIdx.x, k = blockIdx.y % kUmmaQTiles, c0 = blockIdx.y / kUmmaQTiles * V;
+    const int kvh = blockIdx.x % a.num_kv_heads, st = blockIdx.x / a.num_kv_heads;
+    const int s = st / a.tiles_per_seq, tile = st % a.tiles_per_seq;
+    const int G = a.num_q_heads / a.num_kv_heads;
+    const int rows_used = kUmmaRows / G * G;
+    WindowSeq w;
+    window_seq<true>(wa, s, tile, false, w);
+    const int R = k * rows_used + r;
+    if (r >= rows_used || R >= w.n * G) return;
+    const int tiles = (w.nv + kUmmaKeys / kBlock - 1) / (kUmmaKeys / kBlock);
+    const int nparts = (tiles + pw.split_tiles - 1) / pw.split_tiles;
+    if (nparts <= 1) return;
+    const size_t step = (size_t)kUmmaQTiles * kUmmaRows;
+    const size_t slot = ((size_t)blockIdx.x * pw.splits * kUmmaQTiles + k) * kUmmaRows + r;
+    const float2 *__restrict__ ml = pw.ws_ml + slot;
+    const float4 *__restrict__ op = pw.ws_o + (slot - r) * (D / 4) + (size_t)c0 * kUmmaRows + r;
+    float M = -INFINITY, den = 0.f;
+    float4 acc[V];
+#pragma unroll
+    for (int u = 0; u < V; ++u) acc[u] = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 8
+    for (int p = 0; p < nparts; ++p) {
+        const float2 v = ml[p * step];
+        M = fmaxf(M, v.y > 0.f ? v.x : -INFINITY);
+    }
+    for (int p0 = 0; p0 < nparts; p0 += P) {
+        float2 v[P];
+        float4 x[P][V];
+#pragma unroll
+        for (int q = 0; q < P; ++q) {
+            const int p = min(p0 + q, nparts - 1);
+            v[q] = ml[p * step];
+#pragma unroll
+            for (int u = 0; u < V; ++u) x[q][u] = op[p * step * (D / 4) + (size_t)u * kUmmaRows];
+        }
+#pragma unroll
+        for (int q = 0; q < P; ++q) {
+            const float wt = p0 + q < nparts && v[q].y > 0.f ? fast_exp2(v[q].x - M) : 0.f;
+            den += wt * v[q].y;
+#pragma unroll
+            for (int u = 0; u < V; ++u) {
+                acc[u].x += wt * x[q][u].x; acc[u].y += wt * x[q][u].y;
+                acc[u].z += wt * x[q][u].z; acc[u].w += wt * x[q][u].w;
+            }
+        }
+    }
+    const float inv = den > 0.f ? 1.f / den : 0.f;
+    uint16_t *out = reinterpret_cast<uint16_t *>(a.out) +
+                    ((size_t)(w.q0 + R / G) * a.num_q_heads + (size_t)kvh * G + R % G) * D + c0 * 4;
+#pragma unroll
+    for (int u = 0; u < V; u += 2) {
+        const uint2 lo = narrow4(acc[u], inv, T()), hi = narrow4(acc[u + 1], inv, T());
+        *reinterpret_cast<uint4 *>(out + 4 * u) = make_uint4(lo.x, lo.y, hi.x, hi.y);
     }
 }
 

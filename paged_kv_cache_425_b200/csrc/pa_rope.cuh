@@ -60,19 +60,14 @@ __global__ void __launch_bounds__(kRopeThreads) rope_kernel(const __grid_constan
     const bool next = a.rope.interleaved;
     pdl_launch_dependents();
     pdl_wait_prior();
-    long long slot = a.slots[t];
-    if (slot >= a.num_slots) {
-        if (threadIdx.x == 0) flag_error(PA_DEVERR_SLOT);
-        slot = -1;
-    }
     const int heads = a.num_q_heads + 2 * a.num_kv_heads;
     const int units = heads * UNITS;
-    const size_t cache_row = slot < 0 ? 0 : (size_t)(slot / kBlock) * a.num_kv_heads * kBlock + slot % kBlock;
+    long long slot = a.slots[t];  // needed for the stores only
 
     bool ready = false;
     for (int w0 = threadIdx.x; w0 < units || !ready; w0 += kRopeThreads * kRopeUnroll) {
-        uint4 x[kRopeUnroll], y[kRopeUnroll], *dst[kRopeUnroll];
-        int c0[kRopeUnroll], c1[kRopeUnroll];
+        uint4 x[kRopeUnroll], y[kRopeUnroll];
+        int head[kRopeUnroll], c0[kRopeUnroll], c1[kRopeUnroll];
         bool turn[kRopeUnroll];
 #pragma unroll
         for (int r = 0; r < kRopeUnroll; ++r) {
@@ -83,19 +78,11 @@ __global__ void __launch_bounds__(kRopeThreads) rope_kernel(const __grid_constan
             c1[r] = halves ? u + half8 : 2 * u + 1;
             const int hk = h - a.num_q_heads, hv = hk - a.num_kv_heads;
             turn[r] = hv < 0 && c0[r] < 2 * half8;
-            dst[r] = nullptr;
-            if (w >= units || (hk >= 0 && slot < 0)) continue;
-            const uint4 *src;
-            if (hk < 0) {
-                src = a.q + (size_t)t * a.q_stride + (size_t)h * VPR;
-                dst[r] = a.q_out + ((size_t)t * a.num_q_heads + h) * VPR;
-            } else if (hv < 0) {
-                src = a.k + (size_t)t * a.k_stride + (size_t)hk * VPR;
-                dst[r] = a.key_cache + (cache_row + (size_t)hk * kBlock) * VPR;
-            } else {
-                src = a.v + (size_t)t * a.v_stride + (size_t)hv * VPR;
-                dst[r] = a.value_cache + (cache_row + (size_t)hv * kBlock) * VPR;
-            }
+            head[r] = h;
+            if (w >= units) continue;
+            const uint4 *src = hk < 0   ? a.q + (size_t)t * a.q_stride + (size_t)h * VPR
+                               : hv < 0 ? a.k + (size_t)t * a.k_stride + (size_t)hk * VPR
+                                        : a.v + (size_t)t * a.v_stride + (size_t)hv * VPR;
             x[r] = src[c0[r]];
             y[r] = src[c1[r]];
         }
@@ -112,10 +99,17 @@ __global__ void __launch_bounds__(kRopeThreads) rope_kernel(const __grid_constan
             }
             __syncthreads();
             ready = true;
+            if (slot >= a.num_slots) {
+                if (threadIdx.x == 0) flag_error(PA_DEVERR_SLOT);
+                slot = -1;
+            }
         }
+        const size_t cache_row =
+            slot < 0 ? 0 : (size_t)(slot / kBlock) * a.num_kv_heads * kBlock + slot % kBlock;
 #pragma unroll
         for (int r = 0; r < kRopeUnroll; ++r) {
-            if (!dst[r]) continue;
+            const int hk = head[r] - a.num_q_heads, hv = hk - a.num_kv_heads;
+            if (w0 + r * kRopeThreads >= units || (hk >= 0 && slot < 0)) continue;
             if (turn[r]) {
                 uint32_t *xs = reinterpret_cast<uint32_t *>(&x[r]);
                 uint32_t *ys = reinterpret_cast<uint32_t *>(&y[r]);
@@ -131,8 +125,11 @@ __global__ void __launch_bounds__(kRopeThreads) rope_kernel(const __grid_constan
                         rope_turn<T>(xs[e], ys[e], s_cs[8 * c0[r] + 2 * e], s_cs[8 * c0[r] + 2 * e + 1]);
                 }
             }
-            dst[r][c0[r]] = x[r];
-            dst[r][c1[r]] = y[r];
+            uint4 *dst = hk < 0   ? a.q_out + ((size_t)t * a.num_q_heads + head[r]) * VPR
+                         : hv < 0 ? a.key_cache + (cache_row + (size_t)hk * kBlock) * VPR
+                                  : a.value_cache + (cache_row + (size_t)hv * kBlock) * VPR;
+            dst[c0[r]] = x[r];
+            dst[c1[r]] = y[r];
         }
     }
 }

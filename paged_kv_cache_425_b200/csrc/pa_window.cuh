@@ -16,85 +16,176 @@
 // mma.sync tile against the 16 tokens of a block.
 #pragma once
 
+#include <type_traits>
+
 #include "pa_kernels.cuh"
 
 namespace pa {
 
+
 struct WindowArgs {
-    DecodeArgs d;                // num_parts, part_blocks: of the visible blocks
+    DecodeArgs d;                // num_parts, part_blocks: of a run's visible blocks
     const int32_t *query_start;  // chunks only: [S + 1]
     int num_q_tokens;            // rows of q / out
     int max_query_len;           // 1 for decode
     int tile_tokens;             // query tokens that share one list of visible blocks
     int window;                  // >= 1
     int num_sinks;               // >= 0
+    int cluster;                 // CTAs per run, 0: d.num_parts partitions of d.part_blocks
 };
 
-// Query tokens and visible blocks of one sequence.
+// A run of query tokens of one sequence, and the blocks visible to it.
 struct WindowSeq {
-    int q0, n, L;  // first query token, query tokens, context length
-    int lo;        // first token inside any row's window
-    int nsb;       // sink blocks in front of the window's blocks
-    int skip;      // blocks between them, with no visible token
-    int nv;        // visible blocks
+    int q0, n;       // first row of q / out (in tokens), query tokens
+    int first, end;  // positions of the first query token and after the last
+    int lo;          // first token inside any row's window
+    int nsb;         // sink blocks in front of the window's blocks
+    int skip;        // blocks between them, with no visible token
+    int nv;          // visible blocks
     // logical block of visible block v
     __device__ __forceinline__ int block(int v) const { return v < nsb ? v : v + skip; }
 };
 
-__device__ __forceinline__ void window_blocks(WindowSeq &w, int first_pos, int end, int window,
+__device__ __forceinline__ void window_blocks(WindowSeq &w, int first, int end, int window,
                                               int num_sinks) {
-    // visible blocks of queries at first_pos .. end - 1
-    w.lo = max(0, first_pos - window + 1);
+    w.first = first;
+    w.end = end;
+    w.lo = max(0, first - window + 1);
     const int b0 = w.lo / kBlock;
     w.nsb = min((min(num_sinks, end) + kBlock - 1) / kBlock, b0);
     w.skip = b0 - w.nsb;
     w.nv = (end + kBlock - 1) / kBlock - w.skip;
 }
 
-// False when the sequence's query rows lie outside q / out (reported).
+// The query tokens of sequence s's tile (decode: its one token); n = 0 if
+// there are none.  Rows outside q / out and chunks longer than announced are
+// reported and left out.
 template <bool CHUNK>
-__device__ __forceinline__ bool window_seq(const WindowArgs &a, int s, bool report, WindowSeq &w) {
+__device__ __forceinline__ void window_seq(const WindowArgs &a, int s, int tile, bool report,
+                                           WindowSeq &w) {
     if constexpr (!CHUNK) {
+        const int L = clamp_context(a.d, s, report);
         w.q0 = s;
-        w.L = clamp_context(a.d, s, report);
-        w.n = w.L > 0 ? 1 : 0;
+        w.n = L > 0 ? 1 : 0;
+        window_blocks(w, L - w.n, L, a.window, a.num_sinks);
     } else {
         w.q0 = a.query_start[s];
-        w.n = a.query_start[s + 1] - w.q0;
-        w.L = a.d.context_lens[s];
+        w.n = 0;
+        int n = a.query_start[s + 1] - w.q0;
+        int L = a.d.context_lens[s];
         const int cap = a.d.max_blocks_per_seq * kBlock;
-        if (w.q0 < 0 || w.q0 > a.num_q_tokens || w.n > a.num_q_tokens - w.q0) {
-            if (report) flag_error(PA_DEVERR_CONTEXT_LEN);
-            return false;
-        }
-        if (w.L < 0 || w.L > cap || w.n < 0 || w.n > w.L) {
-            if (report) flag_error(PA_DEVERR_CONTEXT_LEN);
-            w.L = min(max(w.L, 0), cap);
-            w.n = min(max(w.n, 0), w.L);
-        }
-        if (w.n > a.max_query_len) {
-            if (report) flag_error(PA_DEVERR_CONTEXT_LEN);
-            return false;
-        }
+        bool bad = L < 0 || L > cap || n < 0 || n > L;
+        L = min(max(L, 0), cap);
+        const bool outside = w.q0 < 0 || w.q0 > a.num_q_tokens || n > a.num_q_tokens - w.q0;
+        n = min(max(n, 0), L);
+        const bool drop = outside || n > a.max_query_len;
+        if (report && (bad || drop)) flag_error(PA_DEVERR_CONTEXT_LEN);
+        const int i0 = tile * a.tile_tokens;
+        if (drop || i0 >= n) return;
+        w.n = min(a.tile_tokens, n - i0);
+        w.q0 += i0;
+        window_blocks(w, L - n + i0, L - n + i0 + w.n, a.window, a.num_sinks);
     }
-    window_blocks(w, w.L - w.n, w.L, a.window, a.num_sinks);
-    return true;
 }
 
-// NT 8-row column tiles: rows of a kv head (tokens x group) <= 8 * NT.
-template <typename T, int D, int NW, int STAGES, int NT, int PB, bool CHUNK>
-__global__ void __launch_bounds__(NW * 32, NT == 1 ? PA_DECODE_MIN_CTAS : 3)
+// ------------------------------------------------------------------ thread-block clusters
+__device__ __forceinline__ void cluster_arrive() {
+    asm volatile("barrier.cluster.arrive.release;" ::: "memory");
+}
+__device__ __forceinline__ void cluster_wait() {
+    asm volatile("barrier.cluster.wait.acquire;" ::: "memory");
+}
+
+// Shared-memory address `addr` of this CTA, in CTA `rank` of the cluster.
+__device__ __forceinline__ uint32_t cluster_addr(uint32_t addr, uint32_t rank) {
+    uint32_t r;
+    asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(addr), "r"(rank));
+    return r;
+}
+
+__device__ __forceinline__ void cluster_store4(uint32_t addr, const float4 &v) {
+    asm volatile("st.shared::cluster.v4.f32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "f"(v.x), "f"(v.y),
+                 "f"(v.z), "f"(v.w)
+                 : "memory");
+}
+
+__device__ __forceinline__ void cluster_store2(uint32_t addr, float x, float y) {
+    asm volatile("st.shared::cluster.v2.f32 [%0], {%1, %2};" ::"r"(addr), "f"(x), "f"(y) : "memory");
+}
+
+// ------------------------------------------------------------------ decode over the visible blocks
+// WarpPipe whose boxes (K and V, D / 64 each) are issued by as many lanes at
+// once: one after the other by one lane they take about 100 cycles each, which
+// a warp with few others beside it waits for.  (With 24 warps per SM nobody
+// waits for them, and one lane is 3 % faster.)
+template <int D, int STAGES>
+struct WindowPipe : WarpPipe<D, STAGES> {
+    using Base = WarpPipe<D, STAGES>;
+    __device__ __forceinline__ void issue(int k) {
+        const int phys = __shfl_sync(0xffffffffu, this->my_phys, k);
+        uint64_t *b = &this->bar[k % STAGES];
+        if (phys >= 0) {
+            if (this->lane == 0) mbar_arrive_expect_tx(b, Base::kStage);
+            __syncwarp();
+            if (this->lane < 2 * (D / 64)) {
+                const int col = this->lane % (D / 64);
+                const bool v = this->lane >= D / 64;
+                fence_proxy_async_smem();
+                tma_load_2d_hint(this->ring + (k % STAGES) * Base::kStage + (v ? Base::kTile : 0) + col * 2048,
+                                 v ? this->tmv : this->tmk, b, col * 64,
+                                 (phys * this->num_kv_heads + this->kvh) * kBlock, this->policy);
+            }
+        } else if (this->lane == 0) {
+            mbar_arrive(b);  // bad id: the stage completes empty
+        }
+    }
+};
+
+constexpr int kMaxCluster = 16;
+
+__device__ __forceinline__ uint2 narrow4(const float4 &v, float inv, __half) {
+    return make_uint2(Mma<__half>::pack(v.x * inv, v.y * inv), Mma<__half>::pack(v.z * inv, v.w * inv));
+}
+__device__ __forceinline__ uint2 narrow4(const float4 &v, float inv, __nv_bfloat16) {
+    return make_uint2(Mma<__nv_bfloat16>::pack(v.x * inv, v.y * inv),
+                      Mma<__nv_bfloat16>::pack(v.z * inv, v.w * inv));
+}
+
+// Grid: x = sequence * Hkv + kv head, y = partition of its visible blocks,
+// z = run of tile_tokens query tokens (chunks).  NT 8-row column tiles: rows of
+// a run (tokens x group) <= 8 * NT.
+//
+// A warp takes every NW-th block of its CTA's blocks, U per step, and has
+// STAGES in flight.  Three shapes:
+//  * many rows (U = 1): 4 warps with one block each (two at head_dim 64), six
+//    CTAs per SM, partitions of PB blocks: the shape that reaches the memory's
+//    bandwidth best once the GPU is full.
+//  * fewer (U = 2, PB = 0: a CTA takes its whole run): 4 warps with three
+//    blocks, two CTAs per SM, for runs that fit in one such wave.  At one block
+//    per step a warp needs about 1300 cycles for the chain from scores to
+//    weights, which only many warps hide; two blocks are two chains.
+//  * few rows (CLUSTER): the gridDim.y CTAs of a run, 8 warps each, form one
+//    thread-block cluster, take an equal share of its blocks each and send
+//    their results to each other's shared memory: one launch, no workspace.
+// Partitions are joined by merge_window_kernel through the workspace.
+template <typename T, int D, int NW, int STAGES, int U, int PB, int NT, bool CHUNK, bool CLUSTER>
+__global__ void __launch_bounds__(NW * 32, U > 1 ? 1 : NT == 1 ? PA_DECODE_MIN_CTAS : 3)
     decode_window_kernel(const __grid_constant__ CUtensorMap tmk,
                          const __grid_constant__ CUtensorMap tmv, const WindowArgs wa) {
-    using Pipe = WarpPipe<D, STAGES>;
+    using Pipe = std::conditional_t<U == 1, WarpPipe<D, STAGES>, WindowPipe<D, STAGES>>;
     const DecodeArgs &a = wa.d;
-    constexpr int KS = D / 16;     // 16-wide steps of the head dim
-    constexpr int RMAX = 8 * NT;   // rows this build handles
+    constexpr int KS = D / 16;          // 16-wide steps of the head dim
+    constexpr int RMAX = 8 * NT;        // rows this build handles
+    constexpr int D4 = D / 4;
     static_assert(RMAX * D * 4 <= STAGES * Pipe::kStage, "combine scratch fits in a warp ring");
-    static_assert(PB <= 32 * NW, "a lane holds one block id");
+    static_assert(kMaxCluster <= D4, "one thread per row and peer sends the row's max and sum");
     extern __shared__ uint8_t dyn_smem[];
     __shared__ __align__(8) uint64_t bars[NW][STAGES];
     __shared__ float s_m[NW][RMAX], s_l[NW][RMAX];
+    // what the cluster's CTAs send here: this CTA's share of the rows' elements
+    // from each of them, and every row's (max, sum)
+    __shared__ __align__(16) float4 r_o[CLUSTER ? RMAX * D4 + kMaxCluster : 1];
+    __shared__ __align__(8) float2 r_ml[CLUSTER ? kMaxCluster * RMAX : 1];
 
     const int part = blockIdx.y, kvh = blockIdx.x % a.num_kv_heads,
               s = blockIdx.x / a.num_kv_heads;
@@ -103,23 +194,26 @@ __global__ void __launch_bounds__(NW * 32, NT == 1 ? PA_DECODE_MIN_CTAS : 3)
     pdl_launch_dependents();
     pdl_wait_prior();
     WindowSeq w;
-    if (!window_seq<CHUNK>(wa, s, part == 0 && kvh == 0 && threadIdx.x == 0, w)) return;
-    const int rows = CHUNK ? w.n * G : G;
-    const int nparts = w.n > 0 ? (w.nv + PB - 1) / PB : 0;
-    if (part >= (nparts > 0 ? nparts : 1)) return;
+    window_seq<CHUNK>(wa, s, blockIdx.z, part == 0 && kvh == 0 && blockIdx.z == 0 && threadIdx.x == 0, w);
     uint16_t *out = reinterpret_cast<uint16_t *>(a.out);
-    // row r of the sequence -> row of q / out
+    // row r of the run -> row of q / out
     auto q_row = [&](int r) {
         return CHUNK ? (size_t)(w.q0 + r / G) * a.num_q_heads + (size_t)kvh * G + r % G
                      : (size_t)s * a.num_q_heads + (size_t)kvh * G + r;
     };
-    if (w.n == 0) {
-        if (!CHUNK)
+    if (w.n == 0) {  // the same for every CTA of a cluster
+        if (!CHUNK && part == 0)
             for (int i = threadIdx.x; i < G * D; i += NW * 32) out[q_row(0) * D + i] = 0;
         return;
     }
-    const int v_begin = part * PB;
-    const int nv_local = min(PB, w.nv - v_begin);
+    if constexpr (CLUSTER) cluster_arrive();  // waited for before the first remote store
+    const int rows = CHUNK ? w.n * G : G;
+    const int share = CLUSTER ? (w.nv + (int)gridDim.y - 1) / (int)gridDim.y
+                              : PB > 0 ? PB : w.nv;  // blocks per CTA
+    const int nparts = (w.nv + share - 1) / share;
+    if (!CLUSTER && part >= nparts) return;
+    const int v_begin = part * share;
+    const int nv_local = max(min(share, w.nv - v_begin), 0);
     const int nk = warp_block_count(nv_local, warp, NW);
 
     Pipe pipe;
@@ -149,13 +243,13 @@ __global__ void __launch_bounds__(NW * 32, NT == 1 ? PA_DECODE_MIN_CTAS : 3)
     // the new token's write (pa_decode_append_window) goes before the load of
     // its block, which is the last visible one: as in decode_mma_kernel
     int k_app = -1;
-    if (!CHUNK && a.k_new != nullptr && a.context_lens[s] == w.L) {
+    if (!CHUNK && a.k_new != nullptr && a.context_lens[s] == w.end) {
         const int li = w.nv - 1 - v_begin;
         if (li >= 0 && li < nv_local && li % NW == warp) k_app = li / NW;
     }
-    if (k_app >= 0 && k_app < issued) append_new_token<D>(a, s, kvh, w.L, lane);
+    if (k_app >= 0 && k_app < issued) append_new_token<D>(a, s, kvh, w.end, lane);
     for (int k = 0; k < issued; ++k) pipe.issue(k);
-    if (k_app >= issued) append_new_token<D>(a, s, kvh, w.L, lane);
+    if (k_app >= issued) append_new_token<D>(a, s, kvh, w.end, lane);
 
     const int g = lane >> 2, c = lane & 3;
     // B operand of S^T = K Q^T: lane holds Q[row = 8 nt + g][16 kk + 2c .. +1] and [.. + 8 ..].
@@ -177,7 +271,7 @@ __global__ void __launch_bounds__(NW * 32, NT == 1 ? PA_DECODE_MIN_CTAS : 3)
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-            for (int j = 0; j < 2; ++j) pos[nt][j] = w.L - w.n + min(nt * 8 + 2 * c + j, rows - 1) / G;
+            for (int j = 0; j < 2; ++j) pos[nt][j] = w.first + min(nt * 8 + 2 * c + j, rows - 1) / G;
     }
     // Running softmax state per (tile nt, row 2c + j), and O^T accumulators:
     // acc[nt][j] holds d = 16 j + g (+8), rows 8 nt + 2c (+1).
@@ -194,48 +288,73 @@ __global__ void __launch_bounds__(NW * 32, NT == 1 ? PA_DECODE_MIN_CTAS : 3)
 
     bool dead = false;
     int k = 0;
-    for (; k < nk; ++k) {
-        if (!pipe.wait(k)) {
+    for (; k < nk; k += U) {
+        bool ok = true;
+#pragma unroll
+        for (int u = 0; u < U; ++u)
+            if (k + u < nk) ok = pipe.wait(k + u) && ok;
+        if (!ok) {
             dead = true;
             break;
         }
-        const int phys = __shfl_sync(0xffffffffu, pipe.my_phys, k);
-        if (phys >= 0) {
-            const int base = w.block(v_begin + warp + k * NW) * kBlock;
+        bool use[U], any = false;
+        int base[U], nvalid[U], h0[U], h1[U];
+        uint8_t *kt[U];
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            use[u] = k + u < nk && __shfl_sync(0xffffffffu, pipe.my_phys, k + u) >= 0;
+            any = any || use[u];
+            base[u] = w.block(v_begin + warp + (k + u) * NW) * kBlock;
             // tokens of the block that no row sees: from nvalid on, and h0 .. h1 - 1
-            const int nvalid = min(kBlock, w.L - base);
-            const int h0 = max(wa.num_sinks - base, 0), h1 = min(w.lo - base, kBlock);
-            uint8_t *kt = pipe.ring + (k % STAGES) * Pipe::kStage;
-            uint8_t *vt = kt + Pipe::kTile;
-            const uint32_t kt_s = smem_addr(kt), vt_s = smem_addr(vt);
-            float sf[NT][4];
+            nvalid[u] = min(kBlock, w.end - base[u]);
+            h0[u] = max(wa.num_sinks - base[u], 0);
+            h1[u] = min(w.lo - base[u], kBlock);
+            kt[u] = pipe.ring + ((k + u) % STAGES) * Pipe::kStage;
+        }
+        if (any) {
+            float sf[U][NT][4];
 #pragma unroll
-            for (int nt = 0; nt < NT; ++nt) sf[nt][0] = sf[nt][1] = sf[nt][2] = sf[nt][3] = 0.f;
+            for (int u = 0; u < U; ++u)
 #pragma unroll
-            for (int kk = 0; kk < KS; ++kk) {
-                uint32_t af[4];
-                ldmatrix_x4(af, kt_s + tile_off(ka_row, 2 * kk + ka_half));
+                for (int nt = 0; nt < NT; ++nt)
+                    sf[u][nt][0] = sf[u][nt][1] = sf[u][nt][2] = sf[u][nt][3] = 0.f;
 #pragma unroll
-                for (int nt = 0; nt < NT; ++nt) Mma<T>::run(sf[nt], af, qf[nt][kk][0], qf[nt][kk][1]);
+            for (int kk = 0; kk < KS; ++kk)
+#pragma unroll
+                for (int u = 0; u < U; ++u) {
+                    // (an unused block's stage holds anything: its scores are masked)
+                    uint32_t af[4];
+                    ldmatrix_x4(af, smem_addr(kt[u]) + tile_off(ka_row, 2 * kk + ka_half));
+#pragma unroll
+                    for (int nt = 0; nt < NT; ++nt)
+                        Mma<T>::run(sf[u][nt], af, qf[nt][kk][0], qf[nt][kk][1]);
+                }
+            // sf[u][nt]: (token g, row 2c), (g, 2c+1), (g+8, 2c), (g+8, 2c+1)
+            bool v0[U], v1[U];
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                v0[u] = use[u] && g < nvalid[u] && !(g >= h0[u] && g < h1[u]);
+                v1[u] = use[u] && g + 8 < nvalid[u] && !(g + 8 >= h0[u] && g + 8 < h1[u]);
             }
-            // sf[nt]: (token g, row 2c), (g, 2c+1), (g+8, 2c), (g+8, 2c+1)
-            const bool v0 = g < nvalid && !(g >= h0 && g < h1);
-            const bool v1 = g + 8 < nvalid && !(g + 8 >= h0 && g + 8 < h1);
-            uint32_t pb[NT][2];
+            uint32_t pb[U][NT][2];
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt) {
-                float p[4];
+                float p[U][4];
 #pragma unroll
                 for (int j = 0; j < 2; ++j) {
-                    bool s0 = v0, s1 = v1;
-                    if constexpr (CHUNK) {
-                        const int k0 = base + g, k1 = base + g + 8, pp = pos[nt][j];
-                        s0 = k0 <= pp && (pp - k0 < wa.window || k0 < wa.num_sinks);
-                        s1 = k1 <= pp && (pp - k1 < wa.window || k1 < wa.num_sinks);
+                    float bm = -INFINITY;
+#pragma unroll
+                    for (int u = 0; u < U; ++u) {
+                        bool s0 = v0[u], s1 = v1[u];
+                        if constexpr (CHUNK) {
+                            const int k0 = base[u] + g, k1 = base[u] + g + 8, pp = pos[nt][j];
+                            s0 = use[u] && k0 <= pp && (pp - k0 < wa.window || k0 < wa.num_sinks);
+                            s1 = use[u] && k1 <= pp && (pp - k1 < wa.window || k1 < wa.num_sinks);
+                        }
+                        p[u][j] = s0 ? sf[u][nt][j] * a.scale_log2 : -INFINITY;
+                        p[u][j + 2] = s1 ? sf[u][nt][j + 2] * a.scale_log2 : -INFINITY;
+                        bm = fmaxf(bm, fmaxf(p[u][j], p[u][j + 2]));
                     }
-                    const float x0 = s0 ? sf[nt][j] * a.scale_log2 : -INFINITY;
-                    const float x1 = s1 ? sf[nt][j + 2] * a.scale_log2 : -INFINITY;
-                    float bm = fmaxf(x0, x1);
                     bm = fmaxf(bm, __shfl_xor_sync(0xffffffffu, bm, 4));
                     bm = fmaxf(bm, __shfl_xor_sync(0xffffffffu, bm, 8));
                     bm = fmaxf(bm, __shfl_xor_sync(0xffffffffu, bm, 16));
@@ -243,9 +362,14 @@ __global__ void __launch_bounds__(NW * 32, NT == 1 ? PA_DECODE_MIN_CTAS : 3)
                     // a chunk's row may see nothing of the blocks so far
                     const float m_ref = CHUNK && m_new == -INFINITY ? 0.f : m_new;
                     const float alpha = fast_exp2(mrow[nt][j] - m_ref);
-                    p[j] = fast_exp2(x0 - m_ref);
-                    p[j + 2] = fast_exp2(x1 - m_ref);
-                    lrow[nt][j] = lrow[nt][j] * alpha + p[j] + p[j + 2];
+                    float sum = 0.f;
+#pragma unroll
+                    for (int u = 0; u < U; ++u) {
+                        p[u][j] = fast_exp2(p[u][j] - m_ref);
+                        p[u][j + 2] = fast_exp2(p[u][j + 2] - m_ref);
+                        sum += p[u][j] + p[u][j + 2];
+                    }
+                    lrow[nt][j] = lrow[nt][j] * alpha + sum;
                     mrow[nt][j] = m_new;
 #pragma unroll
                     for (int jj = 0; jj < KS; ++jj) {
@@ -255,28 +379,40 @@ __global__ void __launch_bounds__(NW * 32, NT == 1 ? PA_DECODE_MIN_CTAS : 3)
                 }
                 // P^T rounded to T for the tensor cores (the sum l keeps it in
                 // f32): at most half a step of T relative per weight
-                pb[nt][0] = movmatrix_trans(Mma<T>::pack(p[0], p[1]));
-                pb[nt][1] = movmatrix_trans(Mma<T>::pack(p[2], p[3]));
-            }
-            if (nvalid < kBlock || h0 < h1) {
-                // rows no query sees may hold anything (NaN included): zero them
-                for (int idx = lane; idx < kBlock * (D / 8); idx += 32) {
-                    const int t = idx / (D / 8), ch = idx % (D / 8);
-                    if (t >= nvalid || (t >= h0 && t < h1))
-                        *reinterpret_cast<uint4 *>(vt + tile_off(t, ch)) = make_uint4(0, 0, 0, 0);
+#pragma unroll
+                for (int u = 0; u < U; ++u) {
+                    pb[u][nt][0] = movmatrix_trans(Mma<T>::pack(p[u][0], p[u][1]));
+                    pb[u][nt][1] = movmatrix_trans(Mma<T>::pack(p[u][2], p[u][3]));
                 }
-                __syncwarp();
             }
 #pragma unroll
-            for (int j = 0; j < KS; ++j) {
-                uint32_t af[4];
-                ldmatrix_x4_trans(af, vt_s + tile_off(va_row, 2 * j + va_half));
+            for (int u = 0; u < U; ++u) {
+                if (!use[u]) continue;
+                uint8_t *vt = kt[u] + Pipe::kTile;
+                if (nvalid[u] < kBlock || h0[u] < h1[u]) {
+                    // rows no query sees may hold anything (NaN included): zero them
+                    for (int idx = lane; idx < kBlock * (D / 8); idx += 32) {
+                        const int t = idx / (D / 8), ch = idx % (D / 8);
+                        if (t >= nvalid[u] || (t >= h0[u] && t < h1[u]))
+                            *reinterpret_cast<uint4 *>(vt + tile_off(t, ch)) = make_uint4(0, 0, 0, 0);
+                    }
+                    __syncwarp();
+                }
+                const uint32_t vt_s = smem_addr(vt);
 #pragma unroll
-                for (int nt = 0; nt < NT; ++nt) Mma<T>::run(acc[nt][j], af, pb[nt][0], pb[nt][1]);
+                for (int j = 0; j < KS; ++j) {
+                    uint32_t af[4];
+                    ldmatrix_x4_trans(af, vt_s + tile_off(va_row, 2 * j + va_half));
+#pragma unroll
+                    for (int nt = 0; nt < NT; ++nt)
+                        Mma<T>::run(acc[nt][j], af, pb[u][nt][0], pb[u][nt][1]);
+                }
             }
         }
         __syncwarp();
-        if (issued < nk) pipe.issue(issued++);
+#pragma unroll
+        for (int u = 0; u < U; ++u)
+            if (issued < nk) pipe.issue(issued++);
     }
     if (dead) pipe.drain(k, issued);
 
@@ -318,28 +454,63 @@ __global__ void __launch_bounds__(NW * 32, NT == 1 ? PA_DECODE_MIN_CTAS : 3)
     __syncthreads();
 
     const uint8_t *rings = align_smem_1024(dyn_smem);
-    for (int idx = threadIdx.x; idx < rows * D; idx += NW * 32) {
-        const int r = idx / D, d = idx % D;
+    const int total = rows * D4;               // float4 pieces of the rows
+    const int ctas = gridDim.y;
+    const int slots = CLUSTER ? (total + ctas - 1) / ctas : 1;  // pieces each CTA joins
+    if constexpr (CLUSTER) cluster_wait();     // every CTA of the cluster runs by now
+    for (int e = threadIdx.x; e < total; e += NW * 32) {
+        const int r = e / D4, d4 = e % D4;
         float M = -INFINITY;
 #pragma unroll
         for (int i = 0; i < NW; ++i)
             if (s_l[i][r] > 0.f) M = fmaxf(M, s_m[i][r]);
-        float den = 0.f, o = 0.f;
+        float den = 0.f;
+        float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
         for (int i = 0; i < NW; ++i) {
             if (s_l[i][r] > 0.f) {
                 const float wt = fast_exp2(s_m[i][r] - M);
+                const float4 x = reinterpret_cast<const float4 *>(rings + i * STAGES * Pipe::kStage)[e];
                 den += wt * s_l[i][r];
-                o += wt * reinterpret_cast<const float *>(rings + i * STAGES * Pipe::kStage)[r * D + d];
+                o.x += wt * x.x; o.y += wt * x.y; o.z += wt * x.z; o.w += wt * x.w;
             }
         }
-        o = den > 0.f ? o / den : 0.f;
-        const size_t row = q_row(r);
-        if (nparts == 1) {
-            out[row * D + d] = narrow1(o, T());
+        const float inv = den > 0.f ? 1.f / den : 0.f;
+        if constexpr (CLUSTER) {
+            // unnormalised, with the CTA's max and sum, to the CTA that joins it
+            cluster_store4(cluster_addr(smem_addr(&r_o[part * slots + e % slots]), e / slots), o);
+            if (d4 < ctas) cluster_store2(cluster_addr(smem_addr(&r_ml[part * RMAX + r]), d4), M, den);
         } else {
-            a.ws_o[(row * a.num_parts + part) * D + d] = o;
-            if (d == 0) a.ws_ml[row * a.num_parts + part] = make_float2(den > 0.f ? M : -INFINITY, den);
+            const size_t row = q_row(r);
+            if (nparts == 1) {
+                *reinterpret_cast<uint2 *>(out + row * D + d4 * 4) = narrow4(o, inv, T());
+            } else {
+                o.x *= inv; o.y *= inv; o.z *= inv; o.w *= inv;
+                reinterpret_cast<float4 *>(a.ws_o)[(row * a.num_parts + part) * D4 + d4] = o;
+                if (d4 == 0)
+                    a.ws_ml[row * a.num_parts + part] = make_float2(den > 0.f ? M : -INFINITY, den);
+            }
+        }
+    }
+    if constexpr (CLUSTER) {
+        cluster_arrive();
+        cluster_wait();
+        for (int i = threadIdx.x; i < slots; i += NW * 32) {
+            const int e = part * slots + i;
+            if (e >= total) break;
+            const int r = e / D4, d4 = e % D4;
+            float M = -INFINITY, den = 0.f;
+            float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+            for (int p = 0; p < ctas; ++p) M = fmaxf(M, r_ml[p * RMAX + r].x);
+            for (int p = 0; p < ctas; ++p) {
+                const float2 ml = r_ml[p * RMAX + r];
+                const float4 x = r_o[p * slots + i];
+                const float wt = ml.y > 0.f ? fast_exp2(ml.x - M) : 0.f;
+                den += wt * ml.y;
+                o.x += wt * x.x; o.y += wt * x.y; o.z += wt * x.z; o.w += wt * x.w;
+            }
+            *reinterpret_cast<uint2 *>(out + q_row(r) * D + d4 * 4) =
+                narrow4(o, den > 0.f ? 1.f / den : 0.f, T());
         }
     }
 }
@@ -404,8 +575,7 @@ __device__ __forceinline__ void merge_row_cta(const DecodeArgs &a, size_t row, i
 
 // Joins the partitions of rows whose visible blocks were split: a row of q per
 // warp, or per CTA when a row can have more than kMergeFew partitions.  Rows
-// share their partitions with the other tokens of their tile (all of the
-// sequence's, in decode_window_kernel).
+// share their partitions with the other tokens of their run of tile_tokens.
 template <typename T, int D, bool CHUNK>
 __global__ void __launch_bounds__(kMergeRows * 32) merge_window_kernel(const WindowArgs wa) {
     const DecodeArgs &a = wa.d;
@@ -418,14 +588,11 @@ __global__ void __launch_bounds__(kMergeRows * 32) merge_window_kernel(const Win
     const int s = (int)(id / per_seq);
     if (s >= a.num_seqs) return;
     WindowSeq w;
-    if (!window_seq<CHUNK>(wa, s, false, w)) return;
-    const int i = (int)(id % per_seq) / a.num_q_heads;
+    int i = (int)(id % per_seq) / a.num_q_heads;
+    const int tile = CHUNK ? i / wa.tile_tokens : 0;
+    i -= tile * wa.tile_tokens;
+    window_seq<CHUNK>(wa, s, tile, false, w);
     if (i >= w.n) return;
-    if constexpr (CHUNK) {
-        const int i0 = i / wa.tile_tokens * wa.tile_tokens;
-        const int i1 = min(w.n - i0, wa.tile_tokens) + i0;
-        window_blocks(w, w.L - w.n + i0, w.L - w.n + i1, wa.window, wa.num_sinks);
-    }
     const int nparts = (w.nv + a.part_blocks - 1) / a.part_blocks;
     if (nparts <= 1) return;
     const size_t row = (size_t)(w.q0 + i) * a.num_q_heads + id % a.num_q_heads;

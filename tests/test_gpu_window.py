@@ -204,11 +204,12 @@ def test_prefill_window_of_few_rows(hq, hkv, d, dtype, window, sinks):
 
 
 @pytest.mark.parametrize("hq,hkv,d,dtype", [(8, 2, 128, wl.BF16), (4, 4, 64, wl.F16), (32, 1, 128, wl.F16)])
-@pytest.mark.parametrize("window", [300, 2000, 20000])
+@pytest.mark.parametrize("window", [1000, 2000, 20000])
 def test_prefill_window_split_over_keys(hq, hkv, d, dtype, window):
     """Few work items: each one's keys go to several CTAs and are joined."""
-    p = Windowed(wl.rng_for(window), [6000], [100], hq, hkv, d, dtype, window, 18)
-    assert pk.prefill_window_workspace_size(1, 100, 100, hq, hkv, d, p.tables.shape[1], window, 18) > 0
+    n = 400
+    p = Windowed(wl.rng_for(window), [6000], [n], hq, hkv, d, dtype, window, 18)
+    assert pk.prefill_window_workspace_size(1, n, n, hq, hkv, d, p.tables.shape[1], window, 18) > 0
     out = run_prefill(p)
     assert pk.get_error() == (0, 0)
     assert_close(out, p)

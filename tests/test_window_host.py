@@ -52,10 +52,11 @@ def test_plain_rotation_matches_complex_numbers():
 def test_workspace_sizes():
     size = pk.decode_window_workspace_size
     assert size(64, 32, 32, 128, 128, 100) == 0                   # one partition sees it all
-    assert size(1, 32, 8, 128, 2048, 8192, 4) > 0
+    assert size(1, 32, 8, 128, 2048, 8192, 4) == 0                # few rows: one cluster each
+    assert size(100, 32, 8, 128, 2048, 8192, 4) > 0
     assert size(64, 32, 32, 128, 1 << 20, 2 ** 31 - 1, 2 ** 31 - 1) > 0
     # the table bounds what a window can see
-    assert size(1, 8, 8, 64, 4, 100000) == size(1, 8, 8, 64, 4, 64)
+    assert size(100, 8, 8, 64, 400, 100000) == size(100, 8, 8, 64, 400, 6400) > 0
     assert size(1, 8, 8, 64, 4, 0) == 0 and size(1, 8, 8, 64, 4, 5, -1) == 0
     pre = pk.prefill_window_workspace_size
     assert pre(16, 8192, 512, 32, 8, 128, 1024, 4096) == 0        # enough work without a split
@@ -90,9 +91,9 @@ def decode_status(**kw):
     (dict(hq=9), pk.PA_ERR_INVALID_ARG), (dict(hq=34), pk.PA_ERR_UNSUPPORTED),
     (dict(d=96), pk.PA_ERR_UNSUPPORTED), (dict(bs=32), pk.PA_ERR_UNSUPPORTED),
     (dict(dtype=2), pk.PA_ERR_UNSUPPORTED), (dict(maxb=(1 << 26) + 1), pk.PA_ERR_UNSUPPORTED),
-    (dict(S=1, window=5000, maxb=1000), pk.PA_ERR_WORKSPACE),
-    (dict(S=1, window=5000, maxb=1000, ws=P, wsb=100), pk.PA_ERR_WORKSPACE),
-    (dict(S=1, window=5000, maxb=1000, ws=ODD, wsb=1 << 30), pk.PA_ERR_WORKSPACE),
+    (dict(S=100, window=5000, maxb=1000), pk.PA_ERR_WORKSPACE),
+    (dict(S=100, window=5000, maxb=1000, ws=P, wsb=100), pk.PA_ERR_WORKSPACE),
+    (dict(S=100, window=5000, maxb=1000, ws=ODD, wsb=1 << 30), pk.PA_ERR_WORKSPACE),
 ])
 def test_decode_window_refusals(change, status):
     assert decode_status(**change) == (status, status)
@@ -100,7 +101,7 @@ def test_decode_window_refusals(change, status):
 
 def test_decode_append_window_refuses_bad_new_rows():
     for kw in (dict(k_new=None), dict(v_new=ODD)):
-        assert decode_status(q=P, S=1, window=5000, maxb=1000, **kw) == (pk.PA_ERR_WORKSPACE,
+        assert decode_status(q=P, S=100, window=5000, maxb=1000, **kw) == (pk.PA_ERR_WORKSPACE,
                                                                         pk.PA_ERR_INVALID_ARG)
 
 
@@ -127,7 +128,7 @@ def prefill_status(**kw):
     (dict(q=ODD), pk.PA_ERR_INVALID_ARG), (dict(out=ODD), pk.PA_ERR_INVALID_ARG),
     (dict(start=None), pk.PA_ERR_INVALID_ARG), (dict(max_len=-1), pk.PA_ERR_INVALID_ARG),
     (dict(maxb=(1 << 26) + 1), pk.PA_ERR_UNSUPPORTED),
-    (dict(S=1, max_len=1, rows=1, window=5000, maxb=1000), pk.PA_ERR_WORKSPACE),
+    (dict(S=100, max_len=1, rows=100, window=5000, maxb=1000), pk.PA_ERR_WORKSPACE),
     (dict(S=1, window=5000, maxb=1000), pk.PA_ERR_WORKSPACE),
 ])
 def test_prefill_window_refusals(change, status):
