@@ -819,25 +819,31 @@ WindowPlan window_plan(int64_t num_seqs, int32_t num_q_tokens, int32_t max_query
     const int64_t tiles =
         (window_visible_blocks(max_blocks_per_seq, (int32_t)std::min<int64_t>(max_query_len, item_tokens),
                                window, num_sinks) + kTileBlocks - 1) / kTileBlocks;
+    // one query tile per item: both warpgroups share its key tiles
+    const bool one = group <= kUmmaRows && max_query_len <= kUmmaRows / group;
     // Few rows keep most of a 256-row item empty.  The decode kernel takes about
-    // 1.5 ns per (run, block) while one wave holds the runs, the other about
-    // 2.4 us per key tile on each of the 148 SMs and 5 us more at its ends; 90
-    // measured shapes choose by that within 20 % of the better one (40 tokens,
-    // window 100: 6.5 us here, 10.3 us there; 32 tokens of 4 heads, window 4096:
-    // 29 us here, 24 us there).
+    // 1.5 ns per (run, block) while the GPU holds the runs at once, the other
+    // about 2.1 us per key tile on each of the 148 SMs (half for one query tile)
+    // and 6 us more at its ends.  Of 90 measured shapes this takes the faster
+    // one or one at most 20 % slower (40 tokens, window 100: 6.3 us here, 10.3
+    // there; 32 tokens of 4 heads, window 4096: 25.5 us here, 17.6 there).
     p.umma = group > kChunkRows ||
              (max_query_len > 1 && (int64_t)max_query_len * group > 8 &&
-              (runs > 2 * kWindowSms || runs * blocks > 3500 + 11 * items * tiles));
+              (runs > kWindowSms * PA_DECODE_MIN_CTAS ||
+               2 * runs * blocks > 8400 + (one ? 11 : 22) * items * tiles));
     if (p.umma) {
         p.tile_tokens = (int)item_tokens;
-        // Key ranges per item, each at least two tiles: the fewest microseconds
-        // over the rounds that 148 CTAs need (2.1 per tile, 2.5 per item), plus
-        // the launch and the traffic of joining them.
+        // Key ranges per item: the fewest microseconds over the rounds that 148
+        // CTAs need (2.1 per tile, half for one query tile, and 3 per item), plus
+        // the launch of the join and its traffic.  Measured (8 items of 33 tiles):
+        // 70 us unsplit, 43 in 2 ranges, 28 in 4, 20.3 in 11, 23 in 17.
+        const double per_tile = one ? 1.05 : 2.1, per_range = one ? 0.03 : 0.06;
         double best = 0;
-        for (int64_t n = 1; n <= 64 && (n == 1 || 2 * n <= tiles + 1); ++n) {
+        for (int64_t n = 1; n <= 64 && n <= tiles; ++n) {
             const int64_t per = (tiles + n - 1) / n, used = (tiles + per - 1) / per;
-            const double cost = (double)((items * used + kWindowSms - 1) / kWindowSms) * (2.1 * per + 2.5) +
-                                (used > 1 ? 3.0 + 0.04 * items * used : 0.0);
+            const double cost =
+                (double)((items * used + kWindowSms - 1) / kWindowSms) * (per_tile * per + 3.0) +
+                (used > 1 ? 3.0 + per_range * items * used + 0.25 * used : 0.0);
             if (n == 1 || cost < best) {
                 best = cost;
                 p.parts = used;

@@ -46,7 +46,11 @@
 // packed into key tiles without a gap (a tile is gathered block by block
 // anyway), and mask each row to its own window.  With few items the tiles of
 // an item are split over several CTAs (pw.splits); each writes its O, max and
-// sum to the workspace and merge_umma_kernel joins them.
+// sum to the workspace and merge_umma_kernel joins them.  An item whose rows
+// fit one query tile (it.one) gives both warpgroups the same rows and every
+// other key tile instead: S_k, P_k and O_k are then those of key tiles
+// k, k + 2, ... and warpgroup 0 joins the two halves at the end, reading O_1
+// from tensor memory.
 //
 // Warp 11 only completes the third warpgroup (setmaxnreg works per
 // warpgroup).  Every wait is bounded; a wait that gives up raises the CTA's abort flag, the
@@ -138,6 +142,7 @@ struct UmmaItem {
     // WIN: first key tile and index of this split, splits with tiles, and the
     // visible blocks (nblk counts those)
     int t0, part, nparts;
+    bool one;  // the second query tile is empty
     WindowSeq w;
 };
 
@@ -204,6 +209,7 @@ __device__ __forceinline__ bool umma_item(const PrefillArgs &a, const PrefillWin
     if constexpr (WIN) {
         window_blocks(it.w, L - n + it.row0 / G, it.nkeys, pw.window, pw.num_sinks);
         it.nblk = it.w.nv;
+        it.one = it.rows_total - it.row0 <= rows_used;
         const int tiles = (it.nblk + kUmmaKeys / kBlock - 1) / (kUmmaKeys / kBlock);
         it.nparts = (tiles + pw.split_tiles - 1) / pw.split_tiles;
         if (it.part >= it.nparts) return false;
@@ -240,8 +246,11 @@ __global__ void __launch_bounds__(kUmmaThreads, 1)
 
     extern __shared__ uint8_t dyn_smem[];
     // 0 q_full, 1-2 k_full, 3-4 k_empty, 5-6 v_full, 7-8 v_empty,
-    // 9-10 s_full[k], 11-12 p_full[k], 13 o_done, 14 drain, 15 q_empty
-    __shared__ __align__(8) uint64_t bar[16];
+    // 9-10 s_full[k], 11-12 p_full[k], 13 o_done, 14 drain, 15 q_empty,
+    // WIN: 16 half_done, 17 half_free
+    constexpr int BARS = WIN ? 18 : 16;
+    __shared__ __align__(8) uint64_t bar[BARS];
+    __shared__ float2 s_half[WIN ? kUmmaRows : 1];  // (max, sum) of warpgroup 1's half
     __shared__ uint32_t s_tmem;
     __shared__ int s_abort;
     __shared__ int s_order[kRankMax];  // sequence of each rank, longest context first
@@ -259,7 +268,8 @@ __global__ void __launch_bounds__(kUmmaThreads, 1)
     pdl_launch_dependents();
     pdl_wait_prior();
     if (warp == 8 && lane == 0) {
-        for (int i = 0; i < 16; ++i) mbar_init(&bar[i], (i == 11 || i == 12) ? 4 : 1);
+        for (int i = 0; i < BARS; ++i)
+            mbar_init(&bar[i], (i == 11 || i == 12 || i >= 16) ? 4 : 1);
         fence_mbar_init();
         s_abort = 0;
     }
@@ -318,11 +328,12 @@ __global__ void __launch_bounds__(kUmmaThreads, 1)
                 if (lane == 0) {
                     if (items > 0) freed = wait_or_abort(q_empty, (items - 1) & 1, abort_flag);
                     if (freed) {
-                        mbar_arrive_expect_tx(q_full, (uint32_t)(kUmmaQTiles * NCH * rows_used * 128));
+                        const int qtiles = WIN && it.one ? 1 : kUmmaQTiles;
+                        mbar_arrive_expect_tx(q_full, (uint32_t)(qtiles * NCH * rows_used * 128));
 #pragma unroll
                         for (int k = 0; k < kUmmaQTiles; ++k)
 #pragma unroll
-                            for (int c = 0; c < NCH; ++c)
+                            for (int c = 0; c < NCH && k < qtiles; ++c)
                                 tma_load_4d(sq + k * QB + c * kUmmaChunk, &tmq, q_full, c * 64, 0,
                                             it.kvh, it.q0 + (it.tile * kUmmaQTiles + k) * TT);
                     }
@@ -372,10 +383,10 @@ __global__ void __launch_bounds__(kUmmaThreads, 1)
             const uint32_t idesc_pv = umma_idesc_f16(FMT, kUmmaRows, D, 1);
             const uint32_t q_addr = smem_addr(sq), k_addr = smem_addr(sk), v_addr = smem_addr(sv);
             bool issued = false;
-            // S_k = Q_k K_g^T, both K-major: a 16-element step is 32 bytes
+            // S_k = Q_q K_g^T (q = k but for items of one query tile), both K-major: a 16-element step is 32 bytes
             // along the swizzled row, the next 64 columns one chunk on
-            auto qk = [&](int k, int g) {
-                const uint32_t qb = q_addr + k * QB, kb = k_addr + (g & 1) * KVB;
+            auto qk = [&](int k, int g, int q) {
+                const uint32_t qb = q_addr + q * QB, kb = k_addr + (g & 1) * KVB;
 #pragma unroll
                 for (int kk = 0; kk < QK_STEPS; ++kk) {
                     const uint32_t off = (kk >> 2) * kUmmaChunk + (kk & 3) * 32;
@@ -398,6 +409,7 @@ __global__ void __launch_bounds__(kUmmaThreads, 1)
             };
             bool ok = true;
             int gt = 0, items = 0;
+            int ck[2] = {0, 0};  // WIN: tiles that went through S_k / P_k
             for (int r = 0; ok; ++r) {
                 const int i = umma_round_item(r);
                 if (i >= total) break;
@@ -407,8 +419,42 @@ __global__ void __launch_bounds__(kUmmaThreads, 1)
                            wait_or_abort(&k_full[gt & 1], (gt >> 1) & 1, abort_flag)))
                     break;
                 tc_fence_after();
-                qk(0, gt);
-                qk(1, gt);
+                if constexpr (WIN) {
+                    if (it.one) {
+                        for (int j = 0; j < 2 && j < it.ntiles && ok; ++j) {
+                            const int g = gt + j;
+                            if (j > 0 && !(ok = wait_or_abort(&k_full[g & 1], (g >> 1) & 1, abort_flag))) break;
+                            tc_fence_after();
+                            qk(j, g, 0);
+                            umma_commit(&k_empty[g & 1]);
+                            if (j + 1 == it.ntiles) umma_commit(q_empty);
+                        }
+                        for (int j = 0; j < it.ntiles && ok; ++j) {
+                            const int g = gt + j, k = j & 1;
+                            if (!(ok = wait_or_abort(&v_full[g & 1], (g >> 1) & 1, abort_flag) &&
+                                       wait_or_abort(&p_full[k], ck[k] & 1, abort_flag)))
+                                break;
+                            ++ck[k];
+                            tc_fence_after();
+                            pv(k, g, j < 2);
+                            umma_commit(&v_empty[g & 1]);
+                            if (j + 2 < it.ntiles) {
+                                if (!(ok = wait_or_abort(&k_full[g & 1], ((g + 2) >> 1) & 1, abort_flag))) break;
+                                tc_fence_after();
+                                qk(k, g + 2, 0);
+                                umma_commit(&k_empty[g & 1]);
+                                if (j + 3 == it.ntiles) umma_commit(q_empty);
+                            }
+                        }
+                        if (!ok) break;
+                        umma_commit(o_done);
+                        gt += it.ntiles;
+                        ++items;
+                        continue;
+                    }
+                }
+                qk(0, gt, 0);
+                qk(1, gt, 1);
                 umma_commit(&k_empty[gt & 1]);
                 if (it.ntiles == 1) umma_commit(q_empty);  // the item's last read of Q
                 for (int j = 0; j < it.ntiles; ++j) {
@@ -416,20 +462,20 @@ __global__ void __launch_bounds__(kUmmaThreads, 1)
                     const uint32_t ph = (g >> 1) & 1;
                     const bool next = j + 1 < it.ntiles;
                     if (!(ok = wait_or_abort(&v_full[b], ph, abort_flag))) break;
-                    if (!(ok = wait_or_abort(&p_full[0], g & 1, abort_flag))) break;
+                    if (!(ok = wait_or_abort(&p_full[0], (WIN ? ck[0]++ : g) & 1, abort_flag))) break;
                     tc_fence_after();
                     pv(0, g, j == 0);
                     if (next) {
                         if (!(ok = wait_or_abort(&k_full[b ^ 1], ((g + 1) >> 1) & 1, abort_flag))) break;
                         tc_fence_after();
-                        qk(0, g + 1);
+                        qk(0, g + 1, 0);
                     }
-                    if (!(ok = wait_or_abort(&p_full[1], g & 1, abort_flag))) break;
+                    if (!(ok = wait_or_abort(&p_full[1], (WIN ? ck[1]++ : g) & 1, abort_flag))) break;
                     tc_fence_after();
                     pv(1, g, j == 0);
                     umma_commit(&v_empty[b]);
                     if (next) {
-                        qk(1, g + 1);
+                        qk(1, g + 1, 1);
                         umma_commit(&k_empty[b ^ 1]);
                         if (j + 2 == it.ntiles) umma_commit(q_empty);
                     }
@@ -463,30 +509,43 @@ __global__ void __launch_bounds__(kUmmaThreads, 1)
         const float sl2 = a.scale_log2;  // > 0 (checked on the host)
         bool dead = false;
         int gt = 0, items = 0;
+        int ck = 0, halves = 0;  // WIN: this warpgroup's S tiles; items of one query tile
         for (int rr = 0; !dead; ++rr) {
             const int i = umma_round_item(rr);
             if (i >= total) break;
             UmmaItem it;
             if (!umma_item<WIN>(a, pw, s_order, i, G, rows_used, ranked, false, it)) continue;
-            const int R = it.row0 + k * rows_used + r;
+            const bool one = WIN && it.one;
+            const int R = it.row0 + (one ? 0 : k * rows_used) + r;
             const bool rvalid = r < rows_used && R < it.rows_total;
             const int qi = rvalid ? R / G : 0, qh = rvalid ? R % G : 0;
             const int pos = rvalid ? it.L - it.n + qi : it.nkeys - 1;  // last key this row sees
             const int live_end = min(it.L, it.nblk * kBlock);  // keys from here on hold no data
             float m_run = kMaskedLogit, l = 0.f;
-            for (int j = 0; j < it.ntiles; ++j) {
+            const int j0 = one ? k : 0, dj = one ? 2 : 1;  // key tiles of this warpgroup
+            for (int j = j0; j < it.ntiles; j += dj) {
                 const int g = gt + j;
                 // blocks of the tile whose id is out of range (read before the wait)
                 uint32_t bad = 0;
+                if constexpr (WIN) {  // one lane per block
+                    const int blk = (it.t0 + j) * 8 + lane;
+                    bool out_of_range = false;
+                    if (lane < 8 && blk < it.nblk) {
+                        const int id = it.trow[it.w.block(blk)];
+                        out_of_range = id < 0 || id >= a.num_blocks;
+                    }
+                    bad = __ballot_sync(FULL, out_of_range);
+                } else {
 #pragma unroll
-                for (int q = 0; q < 8; ++q) {
-                    const int blk = (WIN ? it.t0 + j : j) * 8 + q;
-                    if (blk < it.nblk) {
-                        const int id = it.trow[WIN ? it.w.block(blk) : blk];
-                        if (id < 0 || id >= a.num_blocks) bad |= 1u << q;
+                    for (int q = 0; q < 8; ++q) {
+                        const int blk = j * 8 + q;
+                        if (blk < it.nblk) {
+                            const int id = it.trow[blk];
+                            if (id < 0 || id >= a.num_blocks) bad |= 1u << q;
+                        }
                     }
                 }
-                bool ok = wait_or_abort(&s_full[k], g & 1, abort_flag);
+                bool ok = wait_or_abort(&s_full[k], (WIN ? ck++ : g) & 1, abort_flag);
                 if (!__all_sync(FULL, ok)) {
                     dead = true;
                     break;
@@ -548,7 +607,7 @@ __global__ void __launch_bounds__(kUmmaThreads, 1)
                 if (mx > m_run + kMaxSlack) {
                     alpha = fast_exp2(m_run - mx);
                     m_run = mx;
-                    rescale = j > 0;
+                    rescale = j > j0;
                 }
                 // P = 2^(s * scale_log2 - m), 16-bit, two keys per TMEM column,
                 // over the upper half of S_k (already read)
@@ -595,7 +654,7 @@ __global__ void __launch_bounds__(kUmmaThreads, 1)
                 if constexpr (WIN)  // or that no row of the item sees
                     dead_rows = key0 + kUmmaKeys > it.nkeys || bad || key0 + nsc < it.w.lo ||
                                 (nsc > 0 && vis_a < nsc);
-                if (k == 0 && dead_rows) {
+                if ((k == 0 || one) && dead_rows) {
                     // V rows without data (past the context, never loaded, bad
                     // block) meet P = 0 in the MMA; zero them so that whatever
                     // they hold cannot turn 0 * x into NaN
@@ -634,6 +693,55 @@ __global__ void __launch_bounds__(kUmmaThreads, 1)
                 break;
             }
             tc_fence_after();
+            if constexpr (WIN) {
+                if (one) {
+                    if (k == 1) {  // hand (max, sum) over, and O_1 where it is
+                        s_half[r] = make_float2(m_run, l);
+                        tc_fence_before();
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive(&bar[16]);
+                        // until warpgroup 0 has read both
+                        if (!__all_sync(FULL, wait_or_abort(&bar[17], halves & 1, abort_flag))) {
+                            dead = true;
+                            break;
+                        }
+                        ++halves;
+                        gt += it.ntiles;
+                        ++items;
+                        continue;
+                    }
+                    if (!__all_sync(FULL, wait_or_abort(&bar[16], halves & 1, abort_flag))) {
+                        dead = true;
+                        break;
+                    }
+                    tc_fence_after();
+                    if (it.ntiles > 1) {
+                        const float2 h = s_half[r];
+                        const float m = fmaxf(m_run, h.x);
+                        const float w0 = fast_exp2(m_run - m);
+                        const float w1 = fast_exp2(h.x - m);
+                        m_run = m;
+                        l = l * w0 + h.y * w1;
+                        // O_0 takes both halves, where the rest of the epilogue reads it
+#pragma unroll
+                        for (int c0 = 0; c0 < D; c0 += 32) {
+                            uint32_t o[32], o1[32];
+                            tmem_ld32(t_o + c0, o);
+                            tmem_ld32(t_o + D + c0, o1);
+#pragma unroll
+                            for (int e = 0; e < 32; ++e)
+                                o[e] = __float_as_uint(__uint_as_float(o[e]) * w0 +
+                                                       __uint_as_float(o1[e]) * w1);
+                            tmem_st32(t_o + c0, o);
+                        }
+                        tmem_wait_st();
+                    }
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&bar[17]);
+                    ++halves;
+                }
+            }
             const float inv = l > 0.f ? 1.f / l : 0.f;
             if constexpr (WIN) {
                 if (it.nparts > 1) {  // one of several splits: its share to the workspace
@@ -704,14 +812,14 @@ __global__ void __launch_bounds__(kUmmaThreads, 1)
 }
 
 // Joins the splits of pa_prefill_window's items: block x = item, y = query tile
-// and 4 * kMergeVecs columns; thread r = row r of the tile.  Four splits are
-// in flight per thread.
-constexpr int kMergeVecs = 4;
+// and 4 * kMergeVecs columns; thread r = row r of the tile.  Eight splits
+// are in flight per thread.
+constexpr int kMergeVecs = 2;
 
 template <typename T, int D>
 __global__ void __launch_bounds__(kUmmaRows)
     merge_umma_kernel(const PrefillArgs a, const PrefillWindow pw, const WindowArgs wa) {
-    constexpr int V = kMergeVecs, P = 4;
+    constexpr int V = kMergeVecs, P = 8;
     pdl_launch_dependents();
     pdl_wait_prior();
     const int r = threadIdx.x, k = blockIdx.y % kUmmaQTiles, c0 = blockIdx.y / kUmmaQTiles * V;
@@ -734,11 +842,6 @@ __global__ void __launch_bounds__(kUmmaRows)
     float4 acc[V];
 #pragma unroll
     for (int u = 0; u < V; ++u) acc[u] = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 8
-    for (int p = 0; p < nparts; ++p) {
-        const float2 v = ml[p * step];
-        M = fmaxf(M, v.y > 0.f ? v.x : -INFINITY);
-    }
     for (int p0 = 0; p0 < nparts; p0 += P) {
         float2 v[P];
         float4 x[P][V];
@@ -748,6 +851,16 @@ __global__ void __launch_bounds__(kUmmaRows)
             v[q] = ml[p * step];
 #pragma unroll
             for (int u = 0; u < V; ++u) x[q][u] = op[p * step * (D / 4) + (size_t)u * kUmmaRows];
+        }
+        float m = M;
+#pragma unroll
+        for (int q = 0; q < P; ++q) m = fmaxf(m, v[q].y > 0.f ? v[q].x : -INFINITY);
+        const float old = m == -INFINITY ? 0.f : fast_exp2(M - m);
+        M = m;
+        den *= old;
+#pragma unroll
+        for (int u = 0; u < V; ++u) {
+            acc[u].x *= old; acc[u].y *= old; acc[u].z *= old; acc[u].w *= old;
         }
 #pragma unroll
         for (int q = 0; q < P; ++q) {
