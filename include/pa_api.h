@@ -366,6 +366,31 @@ size_t pa_prefill_window_workspace_size(int32_t num_seqs, int32_t num_q_tokens,
                                         int32_t num_sinks);
 
 /*
+ * pa_window_call - the three windowed calls with their arguments in one
+ * structure, for callers whose foreign-function interface converts argument
+ * by argument (that takes longer than a small call on the GPU).  The same
+ * checks, work and statuses; the structure is read before the call returns.
+ */
+#define PA_WINDOW_DECODE 0
+#define PA_WINDOW_DECODE_APPEND 1
+#define PA_WINDOW_PREFILL 2
+typedef struct {
+    void *out;
+    const void *q, *k_new, *v_new; /* k_new, v_new: decode_append only */
+    void *key_cache, *value_cache;
+    const int32_t *block_tables, *context_lens, *query_start; /* query_start: prefill only */
+    void *workspace, *stream;
+    uint64_t workspace_bytes;
+    int64_t num_blocks;
+    int32_t call; /* PA_WINDOW_* */
+    int32_t window, num_sinks, num_kv_heads, num_seqs, num_q_heads;
+    int32_t num_q_tokens, max_query_len; /* prefill only */
+    int32_t head_dim, block_size, max_blocks_per_seq, dtype;
+    float scale;
+} pa_window_args;
+int pa_window_call(const pa_window_args *args);
+
+/*
  * Rotary positions: which angle each pair of a head's elements turns by.  The
  * caller keeps one per model (pa_rope_init) and passes it to every call.
  *
@@ -418,6 +443,20 @@ int pa_rope_and_cache(void *q_out, const void *q, const void *k, const void *v, 
                       int32_t num_tokens, int32_t num_q_heads, int32_t num_kv_heads,
                       int32_t head_dim, int32_t block_size, int64_t num_blocks, int32_t dtype,
                       void *stream);
+
+/* pa_rope_and_cache with its arguments in one structure (see pa_window_call). */
+typedef struct {
+    void *q_out;
+    const void *q, *k, *v;
+    void *key_cache, *value_cache;
+    const int64_t *slot_mapping;
+    const int32_t *positions;
+    const pa_rope *rope;
+    void *stream;
+    int64_t q_stride, k_stride, v_stride, num_blocks;
+    int32_t num_tokens, num_q_heads, num_kv_heads, head_dim, block_size, dtype;
+} pa_rope_args;
+int pa_rope_call(const pa_rope_args *args);
 
 /*
  * pa_copy_blocks - copy-on-write block copies.

@@ -13,6 +13,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+import struct
 
 import numpy as np
 
@@ -109,6 +110,12 @@ pa_rope_init = _sig("pa_rope_init", ctypes.c_int, ctypes.POINTER(RopeStruct), _P
 pa_rope_and_cache = _sig("pa_rope_and_cache", ctypes.c_int, _P, _P, _P, _P, _P, _P, _P, _P,
                          ctypes.POINTER(RopeStruct), _i64, _i64, _i64, _i32, _i32, _i32, _i32, _i32,
                          _i64, _i32, _P)
+# the same calls with their arguments packed: pa_window_args, pa_rope_args
+pa_window_call = _sig("pa_window_call", ctypes.c_int, ctypes.c_char_p)
+pa_rope_call = _sig("pa_rope_call", ctypes.c_int, ctypes.c_char_p)
+_pack_window = struct.Struct("=12Qq12if4x").pack
+_pack_rope = struct.Struct("=10Q4q6i").pack
+WINDOW_DECODE, WINDOW_DECODE_APPEND, WINDOW_PREFILL = 0, 1, 2
 pa_copy_blocks = _sig("pa_copy_blocks", ctypes.c_int, _P, _P, _P, _i32, _i32, _i32, _i32, _i64,
                       _i32, _P)
 pa_swap_blocks = _sig("pa_swap_blocks", ctypes.c_int, _P, _P, _i64, _P, _P, _i64, _P, _i32, _i32,
@@ -154,9 +161,15 @@ def _check(rc: int, what: str):
 
 
 # ---------------------------------------------------------------- device calls (torch tensors)
+_torch_module = None
+
+
 def _torch():
-    import torch
-    return torch
+    global _torch_module
+    if _torch_module is None:
+        import torch
+        _torch_module = torch
+    return _torch_module
 
 
 def dtype_code(t) -> int:
@@ -294,22 +307,27 @@ def prefill(out, q, key_cache, value_cache, block_tables, context_lens, query_st
 
 
 # ---------------------------------------------------------------- sliding window, rotary positions
-# These calls end within a few microseconds on the GPU, so their checks are
-# kept to plain attribute reads and pass addresses as integers.
-def _ptr(t, name, dtype, dev):
-    """Address of a contiguous tensor of `dtype` on CUDA device `dev`."""
-    if t.dtype is not dtype or t.get_device() != dev or not t.is_contiguous():
-        _dev(t, name, dtype)
+# These calls end within a few microseconds on the GPU, so the binding reads
+# plain attributes, passes addresses as integers and packs the arguments.
+def _need(t, name, dtype, dev):
+    """Raise what is wrong with a tensor that should be contiguous, of `dtype`
+    and on the current CUDA device."""
+    _dev(t, name, dtype)
+    if t.get_device() != dev:
         raise ValueError(f"{name} must be on the current CUDA device {dev}, got {t.device}")
-    return t.data_ptr()
 
 
-def _device_stream(stream):
-    """(current CUDA device, raw stream handle): the launch goes there."""
-    torch = _torch()
-    dev = torch.cuda.current_device()
+def _current_device(t):
+    """The current CUDA device, which is where the launch goes."""
+    dev = t.get_device()
+    if dev < 0 or dev != _torch()._C._cuda_getDevice():
+        raise ValueError(f"tensors must be on the current CUDA device, got {t.device}")
+    return dev
+
+
+def _raw_stream(stream, dev):
     # the handle alone: current_stream() builds a Stream object, over 1 us
-    return dev, torch._C._cuda_getCurrentRawStream(dev) if stream is None else stream.cuda_stream
+    return _torch()._C._cuda_getCurrentRawStream(dev) if stream is None else stream.cuda_stream
 
 
 def _i32_arg(x, name):
@@ -319,27 +337,54 @@ def _i32_arg(x, name):
     return x
 
 
-def _workspace(workspace, dev):
-    if workspace is None:
-        return None, 0
-    return _ptr(workspace, "workspace", workspace.dtype, dev), workspace.nbytes
-
-
-def _window_shapes(out, q, key_cache, value_cache, block_tables, context_lens, num_kv_heads):
-    """Shared checks of the windowed calls -> (rows, Hq, d, block size, num_blocks, S, max_blocks)."""
+def _window(call, what, out, q, k_new, v_new, key_cache, value_cache, block_tables, context_lens,
+            query_start, max_query_len, num_kv_heads, scale, window, num_sinks, workspace, stream):
     shape = key_cache.shape
     nb, hkv, bs, d = shape
-    if value_cache.shape != shape:
-        raise ValueError("key_cache and value_cache must match")
-    if hkv != num_kv_heads:
-        raise ValueError("num_kv_heads does not match the cache")
     rows, hq, dq = q.shape
+    S, maxb = block_tables.shape
+    if value_cache.shape != shape or hkv != num_kv_heads:
+        raise ValueError("key_cache and value_cache must match, with num_kv_heads heads")
     if dq != d or out.shape != q.shape:
         raise ValueError("q / out must be [rows, Hq, d] of the cache dtype")
-    S, maxb = block_tables.shape
     if context_lens.shape != (S,):
         raise ValueError("block_tables must be [S, max_blocks], context_lens [S]")
-    return rows, hq, d, bs, nb, S, maxb
+    dev = _current_device(q)
+    dtype, i32 = q.dtype, _torch().int32
+    tensors = [(out, "out", dtype), (q, "q", dtype), (key_cache, "key_cache", dtype),
+               (value_cache, "value_cache", dtype), (block_tables, "block_tables", i32),
+               (context_lens, "context_lens", i32)]
+    if call == WINDOW_PREFILL:
+        if query_start.shape != (S + 1,):
+            raise ValueError("query_start must be [S + 1]")
+        tensors.append((query_start, "query_start", i32))
+    else:
+        if rows != S:
+            raise ValueError("q must have one row per sequence")
+        if call == WINDOW_DECODE_APPEND:
+            if k_new.shape != (S, hkv, d) or v_new.shape != (S, hkv, d):
+                raise ValueError("k_new and v_new must be [S, Hkv, d] of the cache dtype")
+            tensors += ((k_new, "k_new", dtype), (v_new, "v_new", dtype))
+    ws_ptr = ws_bytes = 0
+    if workspace is not None:
+        tensors.append((workspace, "workspace", workspace.dtype))
+        ws_ptr, ws_bytes = workspace.data_ptr(), workspace.nbytes
+    for t, name, want in tensors:
+        if t.dtype is not want or t.get_device() != dev or not t.is_contiguous():
+            _need(t, name, want, dev)
+    try:
+        args = _pack_window(
+            out.data_ptr(), q.data_ptr(), k_new.data_ptr() if k_new is not None else 0,
+            v_new.data_ptr() if v_new is not None else 0, key_cache.data_ptr(),
+            value_cache.data_ptr(), block_tables.data_ptr(), context_lens.data_ptr(),
+            query_start.data_ptr() if query_start is not None else 0, ws_ptr,
+            _raw_stream(stream, dev), ws_bytes, nb, call, window, num_sinks, hkv, S, hq, rows,
+            max_query_len, d, bs, maxb, dtype_code(q), scale)
+    except (struct.error, OverflowError) as e:
+        raise ValueError(f"{what}: {e}") from None
+    rc = pa_window_call(args)
+    if rc:
+        _check(rc, what)
 
 
 def decode_window_workspace_size(num_seqs: int, num_q_heads: int, num_kv_heads: int, head_dim: int,
@@ -356,46 +401,18 @@ def decode_window(out, q, key_cache, value_cache, block_tables, context_lens, nu
     """decode over a sliding window and the first tokens: the query at position
     p = context_lens[s] - 1 sees token j when p - j < window or j < num_sinks.
     Table entries of blocks without such a token are not read."""
-    rows, hq, d, bs, nb, S, maxb = _window_shapes(out, q, key_cache, value_cache, block_tables,
-                                                  context_lens, num_kv_heads)
-    if rows != S:
-        raise ValueError("q must have one row per sequence")
-    dev, st = _device_stream(stream)
-    i32, dtype = _torch().int32, q.dtype
-    ws_ptr, ws_bytes = _workspace(workspace, dev)
-    _check(pa_decode_window(_ptr(out, "out", dtype, dev), _ptr(q, "q", dtype, dev),
-                            _ptr(key_cache, "key_cache", dtype, dev),
-                            _ptr(value_cache, "value_cache", dtype, dev),
-                            _ptr(block_tables, "block_tables", i32, dev),
-                            _ptr(context_lens, "context_lens", i32, dev),
-                            _i32_arg(window, "window"), _i32_arg(num_sinks, "num_sinks"),
-                            num_kv_heads, scale, S, hq, d, bs, maxb, nb, dtype_code(q), ws_ptr,
-                            ws_bytes, st), "pa_decode_window")
+    _window(WINDOW_DECODE, "pa_decode_window", out, q, None, None, key_cache, value_cache,
+            block_tables, context_lens, None, 1, num_kv_heads, scale, window, num_sinks, workspace,
+            stream)
 
 
 def decode_append_window(out, q, k_new, v_new, key_cache, value_cache, block_tables, context_lens,
                          num_kv_heads: int, scale: float, window: int, num_sinks: int = 0,
                          workspace=None, stream=None):
     """decode_append over a sliding window and the first tokens (decode_window)."""
-    rows, hq, d, bs, nb, S, maxb = _window_shapes(out, q, key_cache, value_cache, block_tables,
-                                                  context_lens, num_kv_heads)
-    if rows != S:
-        raise ValueError("q must have one row per sequence")
-    if k_new.shape != (S, num_kv_heads, d) or v_new.shape != (S, num_kv_heads, d):
-        raise ValueError("k_new and v_new must be [S, Hkv, d] of the cache dtype")
-    dev, st = _device_stream(stream)
-    i32, dtype = _torch().int32, q.dtype
-    ws_ptr, ws_bytes = _workspace(workspace, dev)
-    _check(pa_decode_append_window(_ptr(out, "out", dtype, dev), _ptr(q, "q", dtype, dev),
-                                   _ptr(k_new, "k_new", dtype, dev),
-                                   _ptr(v_new, "v_new", dtype, dev),
-                                   _ptr(key_cache, "key_cache", dtype, dev),
-                                   _ptr(value_cache, "value_cache", dtype, dev),
-                                   _ptr(block_tables, "block_tables", i32, dev),
-                                   _ptr(context_lens, "context_lens", i32, dev),
-                                   _i32_arg(window, "window"), _i32_arg(num_sinks, "num_sinks"),
-                                   num_kv_heads, scale, S, hq, d, bs, maxb, nb, dtype_code(q),
-                                   ws_ptr, ws_bytes, st), "pa_decode_append_window")
+    _window(WINDOW_DECODE_APPEND, "pa_decode_append_window", out, q, k_new, v_new, key_cache,
+            value_cache, block_tables, context_lens, None, 1, num_kv_heads, scale, window,
+            num_sinks, workspace, stream)
 
 
 def prefill_window_workspace_size(num_seqs: int, num_q_tokens: int, max_query_len: int,
@@ -413,23 +430,9 @@ def prefill_window(out, q, key_cache, value_cache, block_tables, context_lens, q
                    num_sinks: int = 0, workspace=None, stream=None):
     """Chunked prefill over a sliding window and the first tokens: the row at
     position p sees token j when j <= p and (p - j < window or j < num_sinks)."""
-    rows, hq, d, bs, nb, S, maxb = _window_shapes(out, q, key_cache, value_cache, block_tables,
-                                                  context_lens, num_kv_heads)
-    if query_start.shape != (S + 1,):
-        raise ValueError("query_start must be [S + 1]")
-    dev, st = _device_stream(stream)
-    i32, dtype = _torch().int32, q.dtype
-    ws_ptr, ws_bytes = _workspace(workspace, dev)
-    _check(pa_prefill_window(_ptr(out, "out", dtype, dev), _ptr(q, "q", dtype, dev),
-                             _ptr(key_cache, "key_cache", dtype, dev),
-                             _ptr(value_cache, "value_cache", dtype, dev),
-                             _ptr(block_tables, "block_tables", i32, dev),
-                             _ptr(context_lens, "context_lens", i32, dev),
-                             _ptr(query_start, "query_start", i32, dev),
-                             _i32_arg(max_query_len, "max_query_len"), _i32_arg(window, "window"),
-                             _i32_arg(num_sinks, "num_sinks"), num_kv_heads, scale, S, hq, rows, d,
-                             bs, maxb, nb, dtype_code(q), ws_ptr, ws_bytes, st),
-           "pa_prefill_window")
+    _window(WINDOW_PREFILL, "pa_prefill_window", out, q, None, None, key_cache, value_cache,
+            block_tables, context_lens, query_start, max_query_len, num_kv_heads, scale, window,
+            num_sinks, workspace, stream)
 
 
 class Rope:
@@ -454,6 +457,7 @@ class Rope:
             num_axes = 1 if axes is None else int(axes.max()) + 1
         self._struct = RopeStruct()
         self._ref = ctypes.byref(self._struct)
+        self._address = ctypes.addressof(self._struct)
         _check(pa_rope_init(self._ref, freq.ctypes.data, None if axes is None else axes.ctypes.data,
                             int(freq.size), int(num_axes), int(bool(interleaved))), "pa_rope_init")
         self.num_pairs = int(freq.size)
@@ -481,25 +485,31 @@ def rope_and_cache(q_out, q, k, v, key_cache, value_cache, slot_mapping, positio
     (any token stride that is a multiple of 8); q_out [T][Hq][d] contiguous
     (q itself if contiguous); positions int32 [rope.num_axes][T];
     slot_mapping int64 [T], negative for padding."""
-    torch = _torch()
-    nb, hkv, bs, d = key_cache.shape
-    if value_cache.shape != key_cache.shape:
+    shape = key_cache.shape
+    nb, hkv, bs, d = shape
+    if value_cache.shape != shape:
         raise ValueError("key_cache and value_cache must match")
     T, hq, _ = q_out.shape
     if slot_mapping.shape != (T,) or positions.shape != (rope.num_axes, T):
         raise ValueError(f"slot_mapping must be [{T}], positions [{rope.num_axes}, {T}]")
+    torch = _torch()
     dtype = key_cache.dtype
-    dev, st = _device_stream(stream)
+    dev = _current_device(key_cache)
+    for t, name, want in ((q_out, "q_out", dtype), (key_cache, "key_cache", dtype),
+                          (value_cache, "value_cache", dtype),
+                          (slot_mapping, "slot_mapping", torch.int64),
+                          (positions, "positions", torch.int32)):
+        if t.dtype is not want or t.get_device() != dev or not t.is_contiguous():
+            _need(t, name, want, dev)
     qp, qs = _rows(q, "q", (T, hq, d), dtype, dev)
     kp, ks = _rows(k, "k", (T, hkv, d), dtype, dev)
     vp, vs = _rows(v, "v", (T, hkv, d), dtype, dev)
-    _check(pa_rope_and_cache(_ptr(q_out, "q_out", dtype, dev), qp, kp, vp,
-                             _ptr(key_cache, "key_cache", dtype, dev),
-                             _ptr(value_cache, "value_cache", dtype, dev),
-                             _ptr(slot_mapping, "slot_mapping", torch.int64, dev),
-                             _ptr(positions, "positions", torch.int32, dev), rope._ref, qs, ks, vs,
-                             T, hq, hkv, d, bs, nb, dtype_code(key_cache), st),
-           "pa_rope_and_cache")
+    rc = pa_rope_call(_pack_rope(q_out.data_ptr(), qp, kp, vp, key_cache.data_ptr(),
+                                 value_cache.data_ptr(), slot_mapping.data_ptr(),
+                                 positions.data_ptr(), rope._address, _raw_stream(stream, dev), qs,
+                                 ks, vs, nb, T, hq, hkv, d, bs, dtype_code(key_cache)))
+    if rc:
+        _check(rc, "pa_rope_and_cache")
 
 
 PREFILL_KERNELS = {"auto": 0, "mma_sync": 1, "tcgen05": 2}

@@ -1239,6 +1239,40 @@ int pa_rope_and_cache(void *q_out, const void *q, const void *k, const void *v, 
                            : launch(rope_kernel<__nv_bfloat16, 64>);
 }
 
+int pa_window_call(const pa_window_args *p) {
+    if (!p) return PA_ERR_INVALID_ARG;
+    switch (p->call) {
+        case PA_WINDOW_DECODE:
+            return pa_decode_window(p->out, p->q, p->key_cache, p->value_cache, p->block_tables,
+                                    p->context_lens, p->window, p->num_sinks, p->num_kv_heads,
+                                    p->scale, p->num_seqs, p->num_q_heads, p->head_dim,
+                                    p->block_size, p->max_blocks_per_seq, p->num_blocks, p->dtype,
+                                    p->workspace, p->workspace_bytes, p->stream);
+        case PA_WINDOW_DECODE_APPEND:
+            return pa_decode_append_window(
+                p->out, p->q, p->k_new, p->v_new, p->key_cache, p->value_cache, p->block_tables,
+                p->context_lens, p->window, p->num_sinks, p->num_kv_heads, p->scale, p->num_seqs,
+                p->num_q_heads, p->head_dim, p->block_size, p->max_blocks_per_seq, p->num_blocks,
+                p->dtype, p->workspace, p->workspace_bytes, p->stream);
+        case PA_WINDOW_PREFILL:
+            return pa_prefill_window(
+                p->out, p->q, p->key_cache, p->value_cache, p->block_tables, p->context_lens,
+                p->query_start, p->max_query_len, p->window, p->num_sinks, p->num_kv_heads,
+                p->scale, p->num_seqs, p->num_q_heads, p->num_q_tokens, p->head_dim, p->block_size,
+                p->max_blocks_per_seq, p->num_blocks, p->dtype, p->workspace, p->workspace_bytes,
+                p->stream);
+        default: return PA_ERR_INVALID_ARG;
+    }
+}
+
+int pa_rope_call(const pa_rope_args *p) {
+    if (!p) return PA_ERR_INVALID_ARG;
+    return pa_rope_and_cache(p->q_out, p->q, p->k, p->v, p->key_cache, p->value_cache,
+                             p->slot_mapping, p->positions, p->rope, p->q_stride, p->k_stride,
+                             p->v_stride, p->num_tokens, p->num_q_heads, p->num_kv_heads,
+                             p->head_dim, p->block_size, p->num_blocks, p->dtype, p->stream);
+}
+
 }  // extern "C"
 
 // ---------------------------------------------------------------- no-allocation decode
