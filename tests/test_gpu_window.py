@@ -230,6 +230,15 @@ def test_prefill_window_of_one_query_tile(hq, hkv, d, dtype, chunk, window, sink
     assert torch.equal(out, run_prefill(p))
 
 
+@pytest.mark.parametrize("group", [17, 43, 100, 128])
+def test_prefill_window_wide_groups(group):
+    """More than 16 query heads per kv head, odd ones among them."""
+    p = Windowed(wl.rng_for(group), [500, 90, 33], [7, 1, 20], group, 1, 64, wl.BF16, 70, 3)
+    out = run_prefill(p)
+    assert pk.get_error() == (0, 0)
+    assert_close(out, p)
+
+
 def test_prefill_window_many_items():
     rng = wl.rng_for(12)
     lens = rng.integers(200, 1500, size=40)

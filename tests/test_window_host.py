@@ -286,3 +286,44 @@ def test_random_trims_keep_the_pool_consistent():
         assert [a.refcount(b) for b in range(200)] == list(count)
         st = a.stats()
         assert st["used_blocks"] == (count > 0).sum() and st["free_blocks"] == 200 - st["used_blocks"]
+
+
+# ---------------------------------------------------------------- the binding's own checks
+def binding_args(**kw):
+    a = dict(out=torch.zeros(2, 4, 64, dtype=torch.float16), q=torch.zeros(2, 4, 64, dtype=torch.float16),
+             kc=torch.zeros(8, 2, 16, 64, dtype=torch.float16), vc=torch.zeros(8, 2, 16, 64, dtype=torch.float16),
+             tbl=torch.zeros(2, 4, dtype=torch.int32), lens=torch.ones(2, dtype=torch.int32), hkv=2)
+    a.update(kw)
+    return a["out"], a["q"], a["kc"], a["vc"], a["tbl"], a["lens"], a["hkv"], 0.1, 16
+
+
+@pytest.mark.parametrize("change", [
+    dict(q=torch.zeros(2, 4, 32, dtype=torch.float16)), dict(out=torch.zeros(2, 5, 64, dtype=torch.float16)),
+    dict(lens=torch.ones(3, dtype=torch.int32)), dict(hkv=4),
+    dict(vc=torch.zeros(8, 2, 16, 32, dtype=torch.float16)),
+    dict(),  # host tensors
+])
+def test_binding_refuses_before_the_library(change):
+    with pytest.raises(ValueError):
+        pk.decode_window(*binding_args(**change))
+
+
+def test_packed_arguments_match_the_structures():
+    """The packed formats are the C structures: the same refusals through both."""
+    def call(window, call=pk.WINDOW_DECODE, maxb=64):
+        return pk.pa_window_call(pk._pack_window(4096, 4096, 0, 0, 4096, 4096, 4096, 4096, 4096, 0, 0, 0, 100,
+                                                 call, window, 4, 2, 0, 8, 300, 100, 64, 16, maxb, 0, 0.1))
+    assert call(64) == pk.PA_OK  # no sequences: nothing to do
+    assert call(0) == pk.PA_ERR_INVALID_ARG and call(64, call=3) == pk.PA_ERR_INVALID_ARG
+    assert call(64, maxb=(1 << 26) + 1) == pk.PA_ERR_UNSUPPORTED
+    assert call(64, call=pk.WINDOW_PREFILL) == pk.PA_OK
+    assert call(-1, call=pk.WINDOW_PREFILL) == pk.PA_ERR_INVALID_ARG
+    rope = pk.Rope(np.ones(32))
+
+    def rope_call(T, d=64, ks=128):
+        return pk.pa_rope_call(pk._pack_rope(4096, 4096, 4096, 4096, 4096, 4096, 4096, 4096, rope._address, 0, 512,
+                                             ks, 128, 10, T, 8, 2, d, 16, 0))
+    assert rope_call(0) == pk.PA_OK and rope_call(-1) == pk.PA_ERR_INVALID_ARG
+    assert rope_call(3, d=96) == pk.PA_ERR_UNSUPPORTED and rope_call(3, ks=129) == pk.PA_ERR_INVALID_ARG
+    assert pk._lib.pa_window_call(None) == pk.PA_ERR_INVALID_ARG
+    assert pk._lib.pa_rope_call(None) == pk.PA_ERR_INVALID_ARG
