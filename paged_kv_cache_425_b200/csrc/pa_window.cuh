@@ -92,6 +92,10 @@ __device__ __forceinline__ void window_seq(const WindowArgs &a, int s, int tile,
 __device__ __forceinline__ void cluster_arrive() {
     asm volatile("barrier.cluster.arrive.release;" ::: "memory");
 }
+// With nothing to publish (the releasing form takes about 1000 cycles).
+__device__ __forceinline__ void cluster_arrive_relaxed() {
+    asm volatile("barrier.cluster.arrive.relaxed;" ::: "memory");
+}
 __device__ __forceinline__ void cluster_wait() {
     asm volatile("barrier.cluster.wait.acquire;" ::: "memory");
 }
@@ -114,29 +118,38 @@ __device__ __forceinline__ void cluster_store2(uint32_t addr, float x, float y) 
 }
 
 // ------------------------------------------------------------------ decode over the visible blocks
-// WarpPipe whose boxes (K and V, D / 64 each) are issued by as many lanes at
-// once: one after the other by one lane they take about 100 cycles each, which
-// a warp with few others beside it waits for.  (With 24 warps per SM nobody
-// waits for them, and one lane is 3 % faster.)
+// WarpPipe that issues several blocks at once, each box (K and V, D / 64 each)
+// from a lane of its own: one after the other by one lane, with a proxy fence
+// per block, a block takes about 500 cycles to issue, which a warp with few
+// others beside it waits for.  (With 24 warps per SM nobody waits for it, and
+// the one lane is 3 % faster.)
 template <int D, int STAGES>
 struct WindowPipe : WarpPipe<D, STAGES> {
     using Base = WarpPipe<D, STAGES>;
-    __device__ __forceinline__ void issue(int k) {
-        const int phys = __shfl_sync(0xffffffffu, this->my_phys, k);
-        uint64_t *b = &this->bar[k % STAGES];
-        if (phys >= 0) {
-            if (this->lane == 0) mbar_arrive_expect_tx(b, Base::kStage);
-            __syncwarp();
-            if (this->lane < 2 * (D / 64)) {
-                const int col = this->lane % (D / 64);
-                const bool v = this->lane >= D / 64;
-                fence_proxy_async_smem();
-                tma_load_2d_hint(this->ring + (k % STAGES) * Base::kStage + (v ? Base::kTile : 0) + col * 2048,
-                                 v ? this->tmv : this->tmk, b, col * 64,
-                                 (phys * this->num_kv_heads + this->kvh) * kBlock, this->policy);
-            }
-        } else if (this->lane == 0) {
-            mbar_arrive(b);  // bad id: the stage completes empty
+    static constexpr int kBoxes = 2 * (D / 64);
+    static_assert(STAGES * kBoxes <= 32, "a lane per box");
+    // Blocks k .. k + n - 1 (n <= STAGES).  `reuse`: the stages were read
+    // before, and those reads go first.
+    __device__ __forceinline__ void issue(int k, int n, bool reuse) {
+        const int sub = this->lane / kBoxes, box = this->lane % kBoxes;
+        const int phys = __shfl_sync(0xffffffffu, this->my_phys, (k + sub) & 31);
+        const bool mine = sub < n;
+        uint64_t *b = &this->bar[(k + sub) % STAGES];
+        if (mine && box == 0) {
+            if (phys >= 0)
+                mbar_arrive_expect_tx(b, Base::kStage);
+            else
+                mbar_arrive(b);  // bad id: the stage completes empty
+        }
+        __syncwarp();
+        if (mine && phys >= 0) {
+            const int col = box % (D / 64);
+            const bool v = box >= D / 64;
+            if (reuse) fence_proxy_async_smem();
+            tma_load_2d_hint(this->ring + ((k + sub) % STAGES) * Base::kStage +
+                                 (v ? Base::kTile : 0) + col * 2048,
+                             v ? this->tmv : this->tmk, b, col * 64,
+                             (phys * this->num_kv_heads + this->kvh) * kBlock, this->policy);
         }
     }
 };
@@ -206,7 +219,7 @@ __global__ void __launch_bounds__(NW * 32, U > 1 ? 1 : NT == 1 ? PA_DECODE_MIN_C
             for (int i = threadIdx.x; i < G * D; i += NW * 32) out[q_row(0) * D + i] = 0;
         return;
     }
-    if constexpr (CLUSTER) cluster_arrive();  // waited for before the first remote store
+    if constexpr (CLUSTER) cluster_arrive_relaxed();  // waited for before the first remote store
     const int rows = CHUNK ? w.n * G : G;
     const int share = CLUSTER ? (w.nv + (int)gridDim.y - 1) / (int)gridDim.y
                               : PB > 0 ? PB : w.nv;  // blocks per CTA
@@ -248,7 +261,10 @@ __global__ void __launch_bounds__(NW * 32, U > 1 ? 1 : NT == 1 ? PA_DECODE_MIN_C
         if (li >= 0 && li < nv_local && li % NW == warp) k_app = li / NW;
     }
     if (k_app >= 0 && k_app < issued) append_new_token<D>(a, s, kvh, w.end, lane);
-    for (int k = 0; k < issued; ++k) pipe.issue(k);
+    if constexpr (U > 1)
+        pipe.issue(0, issued, false);
+    else
+        for (int k = 0; k < issued; ++k) pipe.issue(k);
     if (k_app >= issued) append_new_token<D>(a, s, kvh, w.end, lane);
 
     const int g = lane >> 2, c = lane & 3;
@@ -410,9 +426,13 @@ __global__ void __launch_bounds__(NW * 32, U > 1 ? 1 : NT == 1 ? PA_DECODE_MIN_C
             }
         }
         __syncwarp();
-#pragma unroll
-        for (int u = 0; u < U; ++u)
-            if (issued < nk) pipe.issue(issued++);
+        if constexpr (U > 1) {
+            const int n = min(U, nk - issued);
+            if (n > 0) pipe.issue(issued, n, true);
+            issued += n;
+        } else if (issued < nk) {
+            pipe.issue(issued++);
+        }
     }
     if (dead) pipe.drain(k, issued);
 
