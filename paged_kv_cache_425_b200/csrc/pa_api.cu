@@ -856,13 +856,20 @@ WindowPlan window_plan(int64_t num_seqs, int32_t num_q_tokens, int32_t max_query
     p.tile_tokens = (int)run_tokens;
     p.parts = 1;
     if (runs <= kWindowSms && blocks > kManyWarps) {
-        // A cluster as large as finds room for every run at once (at one CTA
-        // per SM the GPU holds 74, 33, 15 and 7 clusters of 2, 4, 8 and 16; a
-        // second wave doubles the time), while each warp keeps a block.
-        constexpr int kRoom[] = {74, 33, 15, 7};
+        // A cluster as large as finds room for every run at once, while each
+        // warp keeps a block.  At one CTA per SM the GPU holds so many clusters
+        // of that size (its CTAs need SMs of one partition of the GPU; sizes
+        // that hold no more than the next larger one are left out); a second
+        // wave doubles the time.
+        constexpr struct {
+            int ctas, room;
+        } kClusters[] = {{16, 7}, {10, 11}, {9, 15}, {6, 22}, {5, 26}, {4, 33}, {3, 45}, {2, 74}, {1, kWindowSms}};
         int ctas = 1;
-        for (int i = 0; i < 4 && runs <= kRoom[i] && (blocks + ctas - 1) / ctas > kFewWarps; ++i)
-            ctas *= 2;
+        for (const auto &c : kClusters)
+            if (runs <= c.room) {
+                ctas = (int)std::min<int64_t>(c.ctas, (blocks + kFewWarps - 1) / kFewWarps);
+                break;
+            }
         if ((blocks + ctas - 1) / ctas <= kFewBlocks) {
             p.cluster = ctas;
             return p;
