@@ -310,8 +310,10 @@ def prefill(out, q, key_cache, value_cache, block_tables, context_lens, query_st
 # These calls end within a few microseconds on the GPU, so the binding reads
 # plain attributes, passes addresses as integers and packs the arguments.
 def _need(t, name, dtype, dev):
-    """Raise what is wrong with a tensor that should be contiguous, of `dtype`
-    and on the current CUDA device."""
+    """A contiguous tensor of `dtype` on the current CUDA device, or an error
+    that says what it is instead."""
+    if t.dtype is dtype and t.get_device() == dev and t.is_contiguous():
+        return
     _dev(t, name, dtype)
     if t.get_device() != dev:
         raise ValueError(f"{name} must be on the current CUDA device {dev}, got {t.device}")
@@ -351,27 +353,34 @@ def _window(call, what, out, q, k_new, v_new, key_cache, value_cache, block_tabl
         raise ValueError("block_tables must be [S, max_blocks], context_lens [S]")
     dev = _current_device(q)
     dtype, i32 = q.dtype, _torch().int32
-    tensors = [(out, "out", dtype), (q, "q", dtype), (key_cache, "key_cache", dtype),
-               (value_cache, "value_cache", dtype), (block_tables, "block_tables", i32),
-               (context_lens, "context_lens", i32)]
+    ok = (out.dtype is dtype and key_cache.dtype is dtype and value_cache.dtype is dtype
+          and block_tables.dtype is i32 and context_lens.dtype is i32
+          and out.get_device() == dev and key_cache.get_device() == dev
+          and value_cache.get_device() == dev and block_tables.get_device() == dev
+          and context_lens.get_device() == dev and out.is_contiguous() and q.is_contiguous()
+          and key_cache.is_contiguous() and value_cache.is_contiguous()
+          and block_tables.is_contiguous() and context_lens.is_contiguous())
+    if not ok:
+        for t, name, want in ((out, "out", dtype), (q, "q", dtype), (key_cache, "key_cache", dtype),
+                              (value_cache, "value_cache", dtype), (block_tables, "block_tables", i32),
+                              (context_lens, "context_lens", i32)):
+            _need(t, name, want, dev)
     if call == WINDOW_PREFILL:
         if query_start.shape != (S + 1,):
             raise ValueError("query_start must be [S + 1]")
-        tensors.append((query_start, "query_start", i32))
+        _need(query_start, "query_start", i32, dev)
     else:
         if rows != S:
             raise ValueError("q must have one row per sequence")
         if call == WINDOW_DECODE_APPEND:
             if k_new.shape != (S, hkv, d) or v_new.shape != (S, hkv, d):
                 raise ValueError("k_new and v_new must be [S, Hkv, d] of the cache dtype")
-            tensors += ((k_new, "k_new", dtype), (v_new, "v_new", dtype))
+            _need(k_new, "k_new", dtype, dev)
+            _need(v_new, "v_new", dtype, dev)
     ws_ptr = ws_bytes = 0
     if workspace is not None:
-        tensors.append((workspace, "workspace", workspace.dtype))
+        _need(workspace, "workspace", workspace.dtype, dev)
         ws_ptr, ws_bytes = workspace.data_ptr(), workspace.nbytes
-    for t, name, want in tensors:
-        if t.dtype is not want or t.get_device() != dev or not t.is_contiguous():
-            _need(t, name, want, dev)
     try:
         args = _pack_window(
             out.data_ptr(), q.data_ptr(), k_new.data_ptr() if k_new is not None else 0,
@@ -495,12 +504,11 @@ def rope_and_cache(q_out, q, k, v, key_cache, value_cache, slot_mapping, positio
     torch = _torch()
     dtype = key_cache.dtype
     dev = _current_device(key_cache)
-    for t, name, want in ((q_out, "q_out", dtype), (key_cache, "key_cache", dtype),
-                          (value_cache, "value_cache", dtype),
-                          (slot_mapping, "slot_mapping", torch.int64),
-                          (positions, "positions", torch.int32)):
-        if t.dtype is not want or t.get_device() != dev or not t.is_contiguous():
-            _need(t, name, want, dev)
+    _need(q_out, "q_out", dtype, dev)
+    _need(key_cache, "key_cache", dtype, dev)
+    _need(value_cache, "value_cache", dtype, dev)
+    _need(slot_mapping, "slot_mapping", torch.int64, dev)
+    _need(positions, "positions", torch.int32, dev)
     qp, qs = _rows(q, "q", (T, hq, d), dtype, dev)
     kp, ks = _rows(k, "k", (T, hkv, d), dtype, dev)
     vp, vs = _rows(v, "v", (T, hkv, d), dtype, dev)

@@ -800,9 +800,10 @@ constexpr int kChunkRows = 16;  // rows of a run on decode_window_kernel
 constexpr int kFewWarps = 8, kManyWarps = 4, kWindowStages = 3;
 constexpr int kFewBlocks = 32 * kFewWarps, kManyBlocks = 32 * kManyWarps;
 
-WindowPlan window_plan(int64_t num_seqs, int32_t num_q_tokens, int32_t max_query_len, int32_t num_q_heads,
-                       int32_t num_kv_heads, int32_t max_blocks_per_seq, int32_t window,
-                       int32_t num_sinks) {
+// The heads, window and widths were checked: 1 <= group <= kUmmaRows.
+WindowPlan window_plan(int64_t num_seqs, int32_t num_q_tokens, int32_t max_query_len,
+                       int32_t num_q_heads, int32_t num_kv_heads, int32_t max_blocks_per_seq,
+                       int32_t window, int32_t num_sinks) {
     const int group = num_q_heads / num_kv_heads;
     WindowPlan p = {};
     p.ws_rows = (int64_t)num_q_tokens * num_q_heads;
@@ -820,7 +821,7 @@ WindowPlan window_plan(int64_t num_seqs, int32_t num_q_tokens, int32_t max_query
         (window_visible_blocks(max_blocks_per_seq, (int32_t)std::min<int64_t>(max_query_len, item_tokens),
                                window, num_sinks) + kTileBlocks - 1) / kTileBlocks;
     // one query tile per item: both warpgroups share its key tiles
-    const bool one = group <= kUmmaRows && max_query_len <= kUmmaRows / group;
+    const bool one = max_query_len <= kUmmaRows / group;
     // Few rows keep most of a 256-row item empty.  The decode kernel takes about
     // 1.5 ns per (run, block) while the GPU holds the runs at once, the other
     // about 2.1 us per key tile on each of the 148 SMs (half for one query tile)
@@ -969,6 +970,12 @@ int check_window(int32_t window, int32_t num_sinks, int32_t max_blocks_per_seq) 
     return PA_OK;
 }
 
+constexpr int kMaxDecodeGroup = 16;  // as check_decode_args
+bool window_heads_ok(int32_t num_q_heads, int32_t num_kv_heads, int max_group) {
+    return num_kv_heads > 0 && num_q_heads > 0 && num_q_heads % num_kv_heads == 0 &&
+           num_q_heads / num_kv_heads <= max_group;
+}
+
 template <bool CHUNK>
 int window_call(WindowArgs &a, int32_t head_dim, int32_t dtype, const void *key_cache,
                 const void *value_cache, cudaStream_t st) {
@@ -1042,8 +1049,9 @@ size_t pa_decode_window_workspace_size(int32_t num_seqs, int32_t num_q_heads, in
                                        int32_t head_dim, int32_t block_size,
                                        int32_t max_blocks_per_seq, int32_t window,
                                        int32_t num_sinks) {
-    if (num_seqs <= 0 || num_q_heads <= 0 || num_kv_heads <= 0 || head_dim <= 0 ||
-        block_size != kBlock || max_blocks_per_seq <= 0 || window < 1 || num_sinks < 0)
+    if (num_seqs <= 0 || !window_heads_ok(num_q_heads, num_kv_heads, kMaxDecodeGroup) ||
+        head_dim <= 0 || block_size != kBlock || max_blocks_per_seq <= 0 ||
+        check_window(window, num_sinks, max_blocks_per_seq) != PA_OK)
         return 0;
     return window_workspace(window_plan(num_seqs, num_seqs, 1, num_q_heads, num_kv_heads,
                                         max_blocks_per_seq, window, num_sinks),
@@ -1081,9 +1089,10 @@ size_t pa_prefill_window_workspace_size(int32_t num_seqs, int32_t num_q_tokens,
                                         int32_t num_kv_heads, int32_t head_dim, int32_t block_size,
                                         int32_t max_blocks_per_seq, int32_t window,
                                         int32_t num_sinks) {
-    if (num_seqs <= 0 || num_q_tokens <= 0 || max_query_len <= 0 || num_kv_heads <= 0 ||
-        num_q_heads < num_kv_heads || num_q_heads / num_kv_heads > kUmmaRows || head_dim <= 0 ||
-        block_size != kBlock || max_blocks_per_seq <= 0 || window < 1 || num_sinks < 0)
+    if (num_seqs <= 0 || num_q_tokens <= 0 || max_query_len <= 0 ||
+        !window_heads_ok(num_q_heads, num_kv_heads, kUmmaRows) || head_dim <= 0 ||
+        block_size != kBlock || max_blocks_per_seq <= 0 ||
+        check_window(window, num_sinks, max_blocks_per_seq) != PA_OK)
         return 0;
     max_query_len = std::min(max_query_len, num_q_tokens);
     return window_workspace(window_plan(num_seqs, num_q_tokens, max_query_len, num_q_heads,

@@ -22,7 +22,6 @@
 
 namespace pa {
 
-
 struct WindowArgs {
     DecodeArgs d;                // num_parts, part_blocks: of a run's visible blocks
     const int32_t *query_start;  // chunks only: [S + 1]

@@ -65,6 +65,14 @@ def test_workspace_sizes():
     assert pre(1, 5, 5, 6, 0, 64, 8, 5) == 0 and pre(1, 5, 5, 512, 1, 64, 8, 5) == 0
     with pytest.raises(ValueError):
         size(1, 8, 8, 64, 4, 2 ** 31)
+    # head counts no call accepts: no plan, and no division by zero on the way
+    for hq, hkv in ((4, 8), (0, 4), (300, 1), (7, 2), (-8, 2), (8, -2), (17, 1)):
+        assert size(100, hq, hkv, 64, 1000, 9000) == 0
+    for hq, hkv in ((4, 8), (0, 4), (300, 1), (7, 2), (-8, 2), (8, -2), (129, 1)):
+        assert pre(1, 512, 512, hq, hkv, 64, 1000, 9000) == 0
+    assert pre(1, 512, 512, 128, 1, 64, 1000, 9000) >= 0
+    big = 2 ** 31 - 1
+    assert size(100, 8, 8, 64, big, big, big) == 0 and pre(1, 9, 9, 8, 8, 64, big, big, big) == 0
 
 
 # ---------------------------------------------------------------- refusals (before any launch)
