@@ -50,7 +50,10 @@
 // fit one query tile (it.one) gives both warpgroups the same rows and every
 // other key tile instead: S_k, P_k and O_k are then those of key tiles
 // k, k + 2, ... and warpgroup 0 joins the two halves at the end, reading O_1
-// from tensor memory.
+// from tensor memory.  Measured (bf16, 32 heads on 8, head_dim 128, 4096-token
+// windows): 16 chunks of 512 tokens 515 us, 1.05 PFLOP/s of visible pairs; one
+// chunk of 512 50 us (in two ranges; 72 us unsplit), one of 32 tokens 16 us (25
+// us with an empty second tile).
 //
 // Warp 11 only completes the third warpgroup (setmaxnreg works per
 // warpgroup).  Every wait is bounded; a wait that gives up raises the CTA's abort flag, the

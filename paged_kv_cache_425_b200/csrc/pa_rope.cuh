@@ -12,7 +12,12 @@
 // Memory bound (every q, k, v element is read once and written once; the
 // angles are shared by all heads of a token).  One CTA per token: its threads
 // put their 16-byte loads in flight, some of them compute the token's P angles
-// meanwhile, and after one barrier each thread turns what it loaded.
+// meanwhile, and after one barrier each thread turns what it loaded.  8192
+// tokens of 32 + 8 + 8 heads of 128 (201 MB) take 35.4 us, 0.87 of the measured
+// copy bandwidth; 64 tokens 2.8 us, a launch.  128 threads with three units
+// each were the fastest of six shapes (256 x 2: 49 us, 64 x 6: 36 us, 128 x 6:
+// 41 us); streaming or uncached loads and a tighter register limit gained
+// nothing.
 #pragma once
 
 #include "pa_kernels.cuh"

@@ -179,6 +179,11 @@ __device__ __forceinline__ uint2 narrow4(const float4 &v, float inv, __nv_bfloat
 //  * few rows (CLUSTER): the gridDim.y CTAs of a run, 8 warps each, form one
 //    thread-block cluster, take an equal share of its blocks each and send
 //    their results to each other's shared memory: one launch, no workspace.
+// Measured (bf16, 32 heads on 8, head_dim 128): 128 sequences with 4096-token
+// windows 312 us, 2.16 GB of visible rows at 6.9 TB/s (a copy reaches 6.55; L2
+// keeps a part between calls); 32 with 512-token windows, one wave, 10.9 us (15.8
+// in partitions); one with an 8192-token window in clusters of ten 10.4 us (13.5
+// in partitions).
 // Partitions are joined by merge_window_kernel through the workspace.
 template <typename T, int D, int NW, int STAGES, int U, int PB, int NT, bool CHUNK, bool CLUSTER>
 __global__ void __launch_bounds__(NW * 32, U > 1 ? 1 : NT == 1 ? PA_DECODE_MIN_CTAS : 3)
