@@ -176,7 +176,7 @@ __device__ __forceinline__ uint2 narrow4(const float4 &v, float inv, __nv_bfloat
 //    blocks, two CTAs per SM, for runs that fit in one such wave.  At one block
 //    per step a warp needs about 1300 cycles for the chain from scores to
 //    weights, which only many warps hide; two blocks are two chains.
-//  * few rows (CLUSTER): the gridDim.y CTAs of a run, 8 warps each, form one
+//  * few rows (CLUSTER): the gridDim.y CTAs of a run, 6 or 8 warps each, form one
 //    thread-block cluster, take an equal share of its blocks each and send
 //    their results to each other's shared memory: one launch, no workspace.
 // Measured (bf16, 32 heads on 8, head_dim 128): 128 sequences with 4096-token
