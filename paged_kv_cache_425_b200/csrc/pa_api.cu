@@ -786,6 +786,7 @@ int64_t window_visible_blocks(int32_t max_blocks_per_seq, int32_t queries, int32
 // prefill_umma_kernel (umma; `parts` ranges of split_tiles key tiles).
 struct WindowPlan {
     bool umma;
+    bool warp_runs;
     int tile_tokens, cluster, part_blocks, split_tiles;
     int64_t parts;
     // rows of the workspace, each with `parts` partial results
@@ -888,6 +889,13 @@ WindowPlan window_plan(int64_t num_seqs, int32_t num_q_tokens, int32_t max_query
         p.part_blocks = 0;  // one CTA per run, all at once (256 runs of 64 blocks: 24.3 us, split 28.5)
         return p;
     }
+    // more runs than a wave of CTAs holds, of a few blocks each (7360 runs: 1 block
+    // 18 us, 40 as a CTA per run; 2 blocks 26 and 42, 6 blocks 57 and 65, 8 blocks
+    // 84 and 74)
+    if (runs > kWindowSms * PA_DECODE_MIN_CTAS && blocks <= 6) {
+        p.warp_runs = true;
+        return p;
+    }
     // 512-token partitions, or 1024 where that still makes several of a run
     // (1024 runs of 258 blocks: 314 us, 325 with the shorter ones; 384 runs of
     // up to 131: 63.3 and 61.7)
@@ -896,15 +904,17 @@ WindowPlan window_plan(int64_t num_seqs, int32_t num_q_tokens, int32_t max_query
     return p;
 }
 
-template <typename T, int D, int NW, int ST, int U, int PB, int NT, bool CHUNK, bool CLUSTER>
+template <typename T, int D, int NW, int ST, int U, int PB, int NT, bool CHUNK, bool CLUSTER, bool WARP = false>
 int launch_window_kernel(const WindowArgs &a, const CUtensorMap &tmk, const CUtensorMap &tmv,
                          cudaStream_t st) {
     constexpr int SMEM = NW * ST * WarpPipe<D, ST>::kStage + 1024;
-    auto k = decode_window_kernel<T, D, NW, ST, U, PB, NT, CHUNK, CLUSTER>;
+    auto k = decode_window_kernel<T, D, NW, ST, U, PB, NT, CHUNK, CLUSTER, WARP>;
     if (!set_smem(k, SMEM) || (CLUSTER && !allow_cluster16(k))) return PA_ERR_CUDA;
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(a.d.num_seqs * a.d.num_kv_heads, CLUSTER ? a.cluster : a.d.num_parts,
-                       (a.max_query_len + a.tile_tokens - 1) / a.tile_tokens);
+    const int tiles = (a.max_query_len + a.tile_tokens - 1) / a.tile_tokens;
+    cfg.gridDim = dim3(a.d.num_seqs * a.d.num_kv_heads, CLUSTER ? a.cluster : a.d.num_parts, tiles);
+    if (WARP)
+        cfg.gridDim = dim3((unsigned)(((int64_t)a.d.num_seqs * a.d.num_kv_heads * tiles + NW - 1) / NW));
     cfg.blockDim = dim3(NW * 32);
     cfg.dynamicSmemBytes = SMEM;
     cfg.stream = st;
@@ -939,6 +949,8 @@ int launch_window(const WindowArgs &a, const CUtensorMap &tmk, const CUtensorMap
             return launch_window_kernel<T, D, kFewWarps<D>, kFewStages<D>, 2, 0, NT, CHUNK, true>(a, tmk, tmv, st);
         if (a.cluster == 1)
             return launch_window_kernel<T, D, kFewWarps<D>, kFewStages<D>, 2, 0, NT, CHUNK, false>(a, tmk, tmv, st);
+        if (a.warp_runs)
+            return launch_window_kernel<T, D, kManyWarps, kOne, 1, 0, NT, CHUNK, false, true>(a, tmk, tmv, st);
         if (a.d.part_blocks == kPartBlocks)
             return launch_window_kernel<T, D, kManyWarps, kOne, 1, kPartBlocks, NT, CHUNK, false>(a, tmk, tmv, st);
         if (a.d.part_blocks == 2 * kPartBlocks)
@@ -1032,6 +1044,7 @@ int decode_window_call(void *out, const void *q, const void *k_new, const void *
     a.d.max_blocks_per_seq = max_blocks_per_seq;
     if (plan.parts > 65535) return PA_ERR_UNSUPPORTED;
     a.cluster = plan.cluster;
+    a.warp_runs = plan.warp_runs;
     a.d.part_blocks = plan.part_blocks;
     a.d.scale_log2 = scale * 1.4426950408889634f;
     a.d.k_new = append ? k_new : nullptr;
@@ -1144,6 +1157,7 @@ int pa_prefill_window(void *out, const void *q, const void *key_cache, const voi
     if (plan.parts > 65535) return PA_ERR_UNSUPPORTED;
     WindowArgs a = {};
     a.cluster = plan.cluster;
+    a.warp_runs = plan.warp_runs;
     a.d.part_blocks = plan.part_blocks;
     a.d.out = out;
     a.d.q = q;

@@ -30,6 +30,7 @@ struct WindowArgs {
     int tile_tokens;             // query tokens that share one list of visible blocks
     int window;                  // >= 1
     int num_sinks;               // >= 0
+    bool warp_runs;              // a warp per run
     int cluster;                 // CTAs per run, 0: d.num_parts partitions of d.part_blocks
 };
 
@@ -164,7 +165,7 @@ __device__ __forceinline__ uint2 narrow4(const float4 &v, float inv, __nv_bfloat
 }
 
 // Grid: x = sequence * Hkv + kv head, y = partition of its visible blocks,
-// z = run of tile_tokens query tokens (chunks).  NT 8-row column tiles: rows of
+// z = run of tile_tokens query tokens (chunks); WARP: x = NW runs.  NT 8-row column tiles: rows of
 // a run (tokens x group) <= 8 * NT.
 //
 // A warp takes every NW-th block of its CTA's blocks, U per step, and has
@@ -184,8 +185,11 @@ __device__ __forceinline__ uint2 narrow4(const float4 &v, float inv, __nv_bfloat
 // keeps a part between calls); 32 with 512-token windows, one wave, 10.9 us (15.8
 // in partitions); one with an 8192-token window in clusters of ten 10.4 us (13.5
 // in partitions).
+//  * many short runs (WARP, U = 1): a warp takes a whole run, four runs per CTA,
+//    with nothing to join: a CTA per run spends most of its 3 us waiting when the
+//    run is a few blocks (7360 runs of one block: 40 us, 18 here).
 // Partitions are joined by merge_window_kernel through the workspace.
-template <typename T, int D, int NW, int STAGES, int U, int PB, int NT, bool CHUNK, bool CLUSTER>
+template <typename T, int D, int NW, int STAGES, int U, int PB, int NT, bool CHUNK, bool CLUSTER, bool WARP>
 __global__ void __launch_bounds__(NW * 32, U > 1 ? 1 : NT == 1 ? PA_DECODE_MIN_CTAS : 3)
     decode_window_kernel(const __grid_constant__ CUtensorMap tmk,
                          const __grid_constant__ CUtensorMap tmv, const WindowArgs wa) {
@@ -204,14 +208,23 @@ __global__ void __launch_bounds__(NW * 32, U > 1 ? 1 : NT == 1 ? PA_DECODE_MIN_C
     __shared__ __align__(16) float4 r_o[CLUSTER ? RMAX * D4 + kMaxCluster : 1];
     __shared__ __align__(8) float2 r_ml[CLUSTER ? kMaxCluster * RMAX : 1];
 
-    const int part = blockIdx.y, kvh = blockIdx.x % a.num_kv_heads,
-              s = blockIdx.x / a.num_kv_heads;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int part = blockIdx.y;
+    int kvh = blockIdx.x % a.num_kv_heads, s = blockIdx.x / a.num_kv_heads, tile = blockIdx.z;
+    if constexpr (WARP) {  // runs in the order kv head, run of the sequence, sequence
+        const long long id = (long long)blockIdx.x * NW + warp;
+        const int tiles = CHUNK ? (wa.max_query_len + wa.tile_tokens - 1) / wa.tile_tokens : 1;
+        kvh = (int)(id % a.num_kv_heads);
+        tile = (int)(id / a.num_kv_heads % tiles);
+        const long long seq = id / a.num_kv_heads / tiles;
+        if (seq >= a.num_seqs) return;
+        s = (int)seq;
+    }
     const int G = a.num_q_heads / a.num_kv_heads;
     pdl_launch_dependents();
     pdl_wait_prior();
     WindowSeq w;
-    window_seq<CHUNK>(wa, s, blockIdx.z, part == 0 && kvh == 0 && blockIdx.z == 0 && threadIdx.x == 0, w);
+    window_seq<CHUNK>(wa, s, tile, part == 0 && kvh == 0 && tile == 0 && (WARP ? lane : threadIdx.x) == 0, w);
     uint16_t *out = reinterpret_cast<uint16_t *>(a.out);
     // row r of the run -> row of q / out
     auto q_row = [&](int r) {
@@ -220,7 +233,8 @@ __global__ void __launch_bounds__(NW * 32, U > 1 ? 1 : NT == 1 ? PA_DECODE_MIN_C
     };
     if (w.n == 0) {  // the same for every CTA of a cluster
         if (!CHUNK && part == 0)
-            for (int i = threadIdx.x; i < G * D; i += NW * 32) out[q_row(0) * D + i] = 0;
+            for (int i = WARP ? lane : threadIdx.x; i < G * D; i += WARP ? 32 : NW * 32)
+                out[q_row(0) * D + i] = 0;
         return;
     }
     if constexpr (CLUSTER) cluster_arrive_relaxed();  // waited for before the first remote store
@@ -231,7 +245,9 @@ __global__ void __launch_bounds__(NW * 32, U > 1 ? 1 : NT == 1 ? PA_DECODE_MIN_C
     if (!CLUSTER && part >= nparts) return;
     const int v_begin = part * share;
     const int nv_local = max(min(share, w.nv - v_begin), 0);
-    const int nk = warp_block_count(nv_local, warp, NW);
+    constexpr int STEP = WARP ? 1 : NW;  // the warp's k-th block is w0 + k * STEP
+    const int w0 = WARP ? 0 : warp;
+    const int nk = warp_block_count(nv_local, w0, STEP);
 
     Pipe pipe;
     pipe.ring = align_smem_1024(dyn_smem) + warp * STAGES * Pipe::kStage;
@@ -245,7 +261,7 @@ __global__ void __launch_bounds__(NW * 32, U > 1 ? 1 : NT == 1 ? PA_DECODE_MIN_C
     pipe.my_phys = -1;
     if (lane < nk) {
         const int phys =
-            a.block_tables[(size_t)s * a.max_blocks_per_seq + w.block(v_begin + warp + lane * NW)];
+            a.block_tables[(size_t)s * a.max_blocks_per_seq + w.block(v_begin + w0 + lane * STEP)];
         if (phys < 0 || phys >= a.num_blocks)
             flag_error(PA_DEVERR_BLOCK_ID);
         else
@@ -262,7 +278,7 @@ __global__ void __launch_bounds__(NW * 32, U > 1 ? 1 : NT == 1 ? PA_DECODE_MIN_C
     int k_app = -1;
     if (!CHUNK && a.k_new != nullptr && a.context_lens[s] == w.end) {
         const int li = w.nv - 1 - v_begin;
-        if (li >= 0 && li < nv_local && li % NW == warp) k_app = li / NW;
+        if (li >= 0 && li < nv_local && li % STEP == w0) k_app = li / STEP;
     }
     if (k_app >= 0 && k_app < issued) append_new_token<D>(a, s, kvh, w.end, lane);
     if constexpr (U > 1)
@@ -324,7 +340,7 @@ __global__ void __launch_bounds__(NW * 32, U > 1 ? 1 : NT == 1 ? PA_DECODE_MIN_C
         for (int u = 0; u < U; ++u) {
             use[u] = k + u < nk && __shfl_sync(0xffffffffu, pipe.my_phys, k + u) >= 0;
             any = any || use[u];
-            base[u] = w.block(v_begin + warp + (k + u) * NW) * kBlock;
+            base[u] = w.block(v_begin + w0 + (k + u) * STEP) * kBlock;
             // tokens of the block that no row sees: from nvalid on, and h0 .. h1 - 1
             nvalid[u] = min(kBlock, w.end - base[u]);
             h0[u] = max(wa.num_sinks - base[u], 0);
@@ -474,6 +490,18 @@ __global__ void __launch_bounds__(NW * 32, U > 1 ? 1 : NT == 1 ? PA_DECODE_MIN_C
                 s_m[warp][r] = mrow[nt][j];
                 s_l[warp][r] = lrow[nt][j];
             }
+    }
+    if constexpr (WARP) {  // the warp has its rows complete
+        __syncwarp();
+        for (int e = lane; e < rows * D4; e += 32) {
+            const int r = e / D4, d4 = e % D4;
+            const float den = s_l[warp][r];
+            const float4 o = den > 0.f ? reinterpret_cast<const float4 *>(wacc)[e]
+                                       : make_float4(0.f, 0.f, 0.f, 0.f);
+            *reinterpret_cast<uint2 *>(out + q_row(r) * D + d4 * 4) =
+                narrow4(o, den > 0.f ? 1.f / den : 0.f, T());
+        }
+        return;
     }
     __syncthreads();
 

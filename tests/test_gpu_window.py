@@ -124,6 +124,31 @@ def test_decode_window_large_batch():
     assert_close(out, p)
 
 
+@pytest.mark.parametrize("hq,hkv,d,dtype", [(32, 32, 128, wl.BF16), (64, 32, 64, wl.F16), (90, 10, 128, wl.F16)])
+@pytest.mark.parametrize("top,window,sinks", [(1, 5, 0), (60, 16, 1), (900, 40, 5), (96, 5000, 3)])
+def test_decode_window_many_short_runs(hq, hkv, d, dtype, top, window, sinks):
+    """A warp per run: thousands of (sequence, kv head) pairs of a few blocks,
+    empty ones among them, and a last CTA that is not full."""
+    rng = wl.rng_for(top + hq)
+    S = 107 if hkv == 10 else 31
+    lens = rng.integers(0, top + 1, size=S)
+    lens[0] = top
+    p = Windowed(rng, lens, np.minimum(lens, 1), hq, hkv, d, dtype, window, sinks)
+    out, live = run_decode(p)
+    assert_close(out[live], p)
+    assert not out[~live].any()
+
+
+def test_prefill_window_many_short_runs():
+    """Chunks of up to 8 rows per kv head take the same shape."""
+    rng = wl.rng_for(33)
+    lens = rng.integers(1, 80, size=300)
+    p = Windowed(rng, lens, np.minimum(lens, rng.integers(0, 4, size=300)), 8, 4, 64, wl.BF16, 20, 2)
+    out = run_prefill(p, max_len=4)
+    assert pk.get_error() == (0, 0)
+    assert_close(out, p)
+
+
 @pytest.mark.parametrize("hq,hkv,d,dtype", SHAPES)
 def test_decode_append_window_equals_write_then_decode(hq, hkv, d, dtype):
     rng = wl.rng_for(60 + hq)
@@ -155,6 +180,32 @@ def test_decode_append_window_equals_write_then_decode(hq, hkv, d, dtype):
             p.k[s][L - 1] = gh.to_host_bits(k_new)[s]
             p.v[s][L - 1] = gh.to_host_bits(v_new)[s]
     assert_close(out2[torch.from_numpy(lens > 0).cuda()], p)
+
+
+def test_decode_append_window_many_short_runs():
+    rng = wl.rng_for(71)
+    S, hq, hkv, d = 40, 32, 32, 64
+    lens = rng.integers(0, 70, size=S)
+    p = Windowed(rng, lens, np.minimum(lens, 1), hq, hkv, d, wl.F16, 30, 4)
+    t = device(p)
+    live = torch.from_numpy(lens > 0).cuda()
+    q = torch.zeros((S, hq, d), dtype=t["q"].dtype, device="cuda")
+    q[live] = t["q"]
+    k_new, v_new = (gh.to_dev(wl.draw_values(rng, (S, hkv, d), wl.F16), wl.F16) for _ in range(2))
+    slots = np.array([p.tables[s, (L - 1) // BS] * BS + (L - 1) % BS if L else -1
+                      for s, L in enumerate(lens)], np.int64)
+    kc, vc = t["kc"].clone(), t["vc"].clone()
+    pk.reshape_and_cache(k_new, v_new, kc, vc, gh.ints(slots, torch.int64))
+    out = torch.full_like(q, float("nan"))
+    pk.decode_append_window(out, q, k_new, v_new, t["kc"], t["vc"], t["tbl"], t["lens"], hkv, p.scale, 30, 4)
+    torch.cuda.synchronize()
+    assert pk.get_error() == (0, 0)
+    assert torch.equal(kc.view(torch.int16), t["kc"].view(torch.int16))
+    assert torch.equal(vc.view(torch.int16), t["vc"].view(torch.int16))
+    for s, L in enumerate(lens):
+        if L:
+            p.k[s][L - 1], p.v[s][L - 1] = gh.to_host_bits(k_new)[s], gh.to_host_bits(v_new)[s]
+    assert_close(out[live], p)
 
 
 def test_bad_block_ids_count_only_where_something_is_seen():
