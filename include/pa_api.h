@@ -338,13 +338,15 @@ size_t pa_decode_window_workspace_size(int32_t num_seqs, int32_t num_q_heads, in
  * that some row sees must be finite, since rows that do not see it still
  * multiply its value by a zero weight.
  *
- * Chunks of up to 16 query rows per kv head (max_query_len times the group)
- * run on the decode kernel, longer ones on the tcgen05 kernel
- * (pa_prefill_select does not matter here).  Either splits a row's keys when
+ * Short chunks run on the decode kernel, up to 16 query rows at a time, longer
+ * ones on the tcgen05 kernel, whichever the sizes make faster (at most 8 query
+ * rows per kv head always on the first, groups above 16 always on the second;
+ * pa_prefill_select does not matter here).  Either splits a row's keys when
  * there is too little work for the GPU; the parts go to `workspace`
  * (pa_prefill_window_workspace_size bytes for the same arguments, 256-byte
- * aligned; may be NULL when that is 0) and are joined in a fixed order.  Calls
- * that share a workspace must not overlap.
+ * aligned; may be NULL when that is 0) and are joined in a fixed order.  The
+ * size does not grow with every argument: a smaller batch may be split where a
+ * larger one is not.  Calls that share a workspace must not overlap.
  *
  * window and num_sinks as in pa_decode_window.  q and out start on 16-byte
  * boundaries.  PA_ERR_UNSUPPORTED for scale <= 0 or not finite, and for more

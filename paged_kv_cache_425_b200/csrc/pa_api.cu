@@ -804,6 +804,7 @@ constexpr int kFewWarps = D == 128 ? 6 : 8;
 template <int D>
 constexpr int kFewStages = D == 128 ? 4 : 6;
 constexpr int kMinFewWarps = 6, kManyWarps = 4, kManyStages = 3;
+constexpr int kWarpRunBlocks = 6;
 constexpr int kFewBlocks = 32 * kMinFewWarps, kManyBlocks = 32 * kManyWarps;
 
 // The heads, window and widths were checked: 1 <= group <= kUmmaRows.
@@ -834,10 +835,18 @@ WindowPlan window_plan(int64_t num_seqs, int32_t num_q_tokens, int32_t max_query
     // and 6 us more at its ends.  Of 90 measured shapes this takes the faster
     // one or one at most 20 % slower (40 tokens, window 100: 6.3 us here, 10.3
     // there; 32 tokens of 4 heads, window 4096: 25.5 us here, 17.6 there).
+    // Beyond one wave of runs only those of few blocks (a warp each) may stay
+    // there: 4 + 0.9 ns per block a run against 5 or 7 us an item and its tiles (31
+    // x 32 heads x 48 tokens: 21 us here, 43 there).
+    const bool wave = runs <= kWindowSms * PA_DECODE_MIN_CTAS;
+    const bool warp_runs = !wave && blocks <= kWarpRunBlocks;
+    const double rounds = (double)((items + kWindowSms - 1) / kWindowSms);
+    const bool slower =
+        wave ? 2 * runs * blocks > 8400 + (one ? 11 : 22) * items * tiles
+             : !warp_runs || 1e-3 * runs * (4 + 0.9 * blocks) >
+                                 rounds * (one ? 5 + 0.9 * tiles : 7 + 2.1 * tiles);
     p.umma = group > kChunkRows ||
-             (max_query_len > 1 && (int64_t)max_query_len * group > 8 &&
-              (runs > kWindowSms * PA_DECODE_MIN_CTAS ||
-               2 * runs * blocks > 8400 + (one ? 11 : 22) * items * tiles));
+             (max_query_len > 1 && (int64_t)max_query_len * group > 8 && slower);
     if (p.umma) {
         p.tile_tokens = (int)item_tokens;
         // Key ranges per item: the fewest microseconds over the rounds that 148
@@ -892,7 +901,7 @@ WindowPlan window_plan(int64_t num_seqs, int32_t num_q_tokens, int32_t max_query
     // more runs than a wave of CTAs holds, of a few blocks each (7360 runs: 1 block
     // 18 us, 40 as a CTA per run; 2 blocks 26 and 42, 6 blocks 57 and 65, 8 blocks
     // 84 and 74)
-    if (runs > kWindowSms * PA_DECODE_MIN_CTAS && blocks <= 6) {
+    if (warp_runs) {
         p.warp_runs = true;
         return p;
     }

@@ -147,6 +147,12 @@ def test_prefill_window_many_short_runs():
     out = run_prefill(p, max_len=4)
     assert pk.get_error() == (0, 0)
     assert_close(out, p)
+    # and longer ones over short contexts: three runs of rows per sequence and head
+    lens = rng.integers(1, 49, size=31)
+    p = Windowed(rng, lens, np.minimum(lens, rng.integers(0, 60, size=31)), 32, 32, 128, wl.F16, 900, 1)
+    out = run_prefill(p, max_len=48)
+    assert pk.get_error() == (0, 0)
+    assert_close(out, p)
 
 
 @pytest.mark.parametrize("hq,hkv,d,dtype", SHAPES)
