@@ -349,7 +349,8 @@ int launch_prefill_umma(void *out, const void *q, const void *key_cache, const v
                         PrefillArgs *used = nullptr) {
     const int group = num_q_heads / num_kv_heads;
     const int tokens_per_tile = kUmmaRows / group;
-    const int64_t rows_per_cta = (int64_t)kUmmaQTiles * tokens_per_tile * group;
+    const int64_t rows_per_cta =
+        (int64_t)(pw ? pw->qtiles : kUmmaQTiles) * tokens_per_tile * group;
     const int64_t tiles = ((int64_t)max_query_len * group + rows_per_cta - 1) / rows_per_cta;
     PrefillArgs a;
     a.out = out;
@@ -787,7 +788,7 @@ int64_t window_visible_blocks(int32_t max_blocks_per_seq, int32_t queries, int32
 struct WindowPlan {
     bool umma;
     bool warp_runs;
-    int tile_tokens, cluster, part_blocks, split_tiles;
+    int tile_tokens, cluster, part_blocks, qtiles, split_tiles;
     int64_t parts;
     // rows of the workspace, each with `parts` partial results
     int64_t ws_rows;
@@ -820,7 +821,8 @@ WindowPlan window_plan(int64_t num_seqs, int32_t num_q_tokens, int32_t max_query
     const int64_t runs = num_seqs * num_kv_heads * ((max_query_len + run_tokens - 1) / run_tokens);
     const int64_t blocks =
         window_visible_blocks(max_blocks_per_seq, (int32_t)run_tokens, window, num_sinks);
-    // prefill_umma_kernel: items of two query tiles, walked in tiles of 128 keys
+    // prefill_umma_kernel: items of two query tiles (halved below where that is
+    // faster), walked in tiles of 128 keys
     constexpr int kTileBlocks = kUmmaKeys / kBlock;
     const int64_t item_tokens = kUmmaQTiles * (kUmmaRows / group);
     const int64_t items = num_seqs * num_kv_heads * ((max_query_len + item_tokens - 1) / item_tokens);
@@ -848,25 +850,38 @@ WindowPlan window_plan(int64_t num_seqs, int32_t num_q_tokens, int32_t max_query
     p.umma = group > kChunkRows ||
              (max_query_len > 1 && (int64_t)max_query_len * group > 8 && slower);
     if (p.umma) {
-        p.tile_tokens = (int)item_tokens;
-        // Key ranges per item: the fewest microseconds over the rounds that 148
-        // CTAs need (2.1 per tile, half for one query tile, and 3 per item), plus
-        // the launch of the join and its traffic.  Measured (8 items of 33 tiles):
-        // 70 us unsplit, 43 in 2 ranges, 28 in 4, 20.3 in 11, 23 in 17.
-        const double per_tile = one ? 1.05 : 2.1, per_range = one ? 0.03 : 0.06;
+        // Query tiles and key ranges per item: the fewest microseconds over the
+        // rounds that 148 CTAs need (2.1 per key tile, half for one query tile, and
+        // 3 per item), plus the launch of the join and its traffic.  Measured: 8
+        // items of 33 tiles 70 us unsplit, 43 in 2 ranges, 28 in 4, 20.3 in 11, 23
+        // in 17; 64 items of 33 tiles 72 us, 51 in 2 ranges, 47 as 128 of one
+        // query tile.
         double best = 0;
-        for (int64_t n = 1; n <= 64 && n <= tiles; ++n) {
-            const int64_t per = (tiles + n - 1) / n, used = (tiles + per - 1) / per;
-            const double cost =
-                (double)((items * used + kWindowSms - 1) / kWindowSms) * (per_tile * per + 3.0) +
-                (used > 1 ? 3.0 + per_range * items * used + 0.25 * used : 0.0);
-            if (n == 1 || cost < best) {
-                best = cost;
-                p.parts = used;
-                p.split_tiles = (int)per;
+        for (int qtiles = kUmmaQTiles; qtiles >= 1; --qtiles) {
+            const int64_t tokens = qtiles * (kUmmaRows / group);
+            const int64_t count =
+                num_seqs * num_kv_heads * ((max_query_len + tokens - 1) / tokens);
+            const int64_t t = (window_visible_blocks(max_blocks_per_seq,
+                                                     (int32_t)std::min<int64_t>(max_query_len, tokens),
+                                                     window, num_sinks) + kTileBlocks - 1) / kTileBlocks;
+            const bool single = one || qtiles == 1;
+            const double per_tile = single ? 1.05 : 2.1, per_range = single ? 0.03 : 0.06;
+            for (int64_t n = 1; n <= 64 && n <= t; ++n) {
+                const int64_t per = (t + n - 1) / n, used = (t + per - 1) / per;
+                const double cost =
+                    (double)((count * used + kWindowSms - 1) / kWindowSms) * (per_tile * per + 3.0) +
+                    (used > 1 ? 3.0 + per_range * count * used + 0.25 * used : 0.0);
+                if (p.parts == 0 || cost < best) {
+                    best = cost;
+                    p.qtiles = qtiles;
+                    p.tile_tokens = (int)tokens;
+                    p.parts = used;
+                    p.split_tiles = (int)per;
+                    p.ws_rows = count * kUmmaQTiles * kUmmaRows;
+                }
             }
+            if (one) break;  // a second query tile would be empty either way
         }
-        p.ws_rows = items * kUmmaQTiles * kUmmaRows;
         return p;
     }
     p.tile_tokens = (int)run_tokens;
@@ -1193,6 +1208,7 @@ int pa_prefill_window(void *out, const void *q, const void *key_cache, const voi
     pw.window = window;
     pw.num_sinks = num_sinks;
     pw.max_query_len = max_query_len;
+    pw.qtiles = plan.qtiles;
     pw.splits = (int)plan.parts;
     pw.split_tiles = plan.split_tiles;
     pw.ws_o = reinterpret_cast<float4 *>(a.d.ws_o);

@@ -47,13 +47,14 @@
 // anyway), and mask each row to its own window.  With few items the tiles of
 // an item are split over several CTAs (pw.splits); each writes its O, max and
 // sum to the workspace and merge_umma_kernel joins them.  An item whose rows
-// fit one query tile (it.one) gives both warpgroups the same rows and every
+// fit one query tile (it.one; all of them with pw.qtiles = 1, twice as many
+// items at half the time each) gives both warpgroups the same rows and every
 // other key tile instead: S_k, P_k and O_k are then those of key tiles
 // k, k + 2, ... and warpgroup 0 joins the two halves at the end, reading O_1
 // from tensor memory.  Measured (bf16, 32 heads on 8, head_dim 128, 4096-token
 // windows): 16 chunks of 512 tokens 515 us, 1.05 PFLOP/s of visible pairs; one
-// chunk of 512 50 us (in two ranges; 72 us unsplit), one of 32 tokens 16 us (25
-// us with an empty second tile).
+// chunk of 512 47 us in items of one query tile (51 us in two key ranges,
+// 72 us neither), one of 32 tokens 16 us (25 us with an empty second tile).
 //
 // Warp 11 only completes the third warpgroup (setmaxnreg works per
 // warpgroup).  Every wait is bounded; a wait that gives up raises the CTA's abort flag, the
@@ -152,6 +153,7 @@ struct UmmaItem {
 // Window of a pa_prefill_window call (unused otherwise).
 struct PrefillWindow {
     int window, num_sinks, max_query_len;
+    int qtiles;               // query tiles per item, 1 or 2
     int splits, split_tiles;  // key-tile ranges per item, tiles in each
     // with more than one split: [item][splits][query tile][D / 4][128 rows] of
     // four elements each, and (max, sum) [item][splits][query tile][128]; rows
@@ -203,16 +205,17 @@ __device__ __forceinline__ bool umma_item(const PrefillArgs &a, const PrefillWin
     it.n = n;
     it.L = L;
     it.rows_total = n * G;
-    it.row0 = it.tile * kUmmaQTiles * rows_used;
+    const int qtiles = WIN ? pw.qtiles : kUmmaQTiles;
+    it.row0 = it.tile * qtiles * rows_used;
     if (it.row0 >= it.rows_total) return false;
-    const int last_row = min(it.rows_total, it.row0 + kUmmaQTiles * rows_used) - 1;
+    const int last_row = min(it.rows_total, it.row0 + qtiles * rows_used) - 1;
     it.nkeys = L - n + last_row / G + 1;
     it.nblk = (it.nkeys + kBlock - 1) / kBlock;
     it.ntiles = (it.nkeys + kUmmaKeys - 1) / kUmmaKeys;
     if constexpr (WIN) {
         window_blocks(it.w, L - n + it.row0 / G, it.nkeys, pw.window, pw.num_sinks);
         it.nblk = it.w.nv;
-        it.one = it.rows_total - it.row0 <= rows_used;
+        it.one = last_row - it.row0 < rows_used;
         const int tiles = (it.nblk + kUmmaKeys / kBlock - 1) / (kUmmaKeys / kBlock);
         it.nparts = (tiles + pw.split_tiles - 1) / pw.split_tiles;
         if (it.part >= it.nparts) return false;
@@ -338,7 +341,7 @@ __global__ void __launch_bounds__(kUmmaThreads, 1)
 #pragma unroll
                             for (int c = 0; c < NCH && k < qtiles; ++c)
                                 tma_load_4d(sq + k * QB + c * kUmmaChunk, &tmq, q_full, c * 64, 0,
-                                            it.kvh, it.q0 + (it.tile * kUmmaQTiles + k) * TT);
+                                            it.kvh, it.q0 + (it.tile * (WIN ? pw.qtiles : kUmmaQTiles) + k) * TT);
                     }
                 }
                 ok = __shfl_sync(FULL, freed, 0);

@@ -260,14 +260,15 @@ def test_prefill_window_of_few_rows(hq, hkv, d, dtype, window, sinks):
     assert_close(out, p)
 
 
-@pytest.mark.parametrize("hq,hkv,d,dtype", [(8, 2, 128, wl.BF16), (4, 4, 64, wl.F16), (32, 1, 128, wl.F16)])
+@pytest.mark.parametrize("hq,hkv,d,dtype,n", [(8, 2, 128, wl.BF16, 400), (4, 4, 64, wl.F16, 400),
+                                              (32, 1, 128, wl.F16, 400), (32, 1, 128, wl.F16, 100),
+                                              (6, 2, 64, wl.BF16, 333)])
 @pytest.mark.parametrize("window", [1000, 2000, 20000])
-def test_prefill_window_split_over_keys(hq, hkv, d, dtype, window):
+def test_prefill_window_split_over_keys(hq, hkv, d, dtype, n, window):
     """Few work items: each one's keys go to several CTAs and are joined."""
-    n = 400
     p = Windowed(wl.rng_for(window), [6000], [n], hq, hkv, d, dtype, window, 18)
     size = pk.prefill_window_workspace_size(1, n, n, hq, hkv, d, p.tables.shape[1], window, 18)
-    assert size > 0 or window == 1000
+    assert size > 0 or window == 1000 or n * hq // hkv > 3200     # enough items of one query tile
     out = run_prefill(p)
     assert pk.get_error() == (0, 0)
     assert_close(out, p)
@@ -281,6 +282,18 @@ def test_prefill_window_of_one_query_tile(hq, hkv, d, dtype, chunk, window, sink
     """At most 128 rows per kv head over many keys: the key tiles are shared out."""
     p = Windowed(wl.rng_for(window + chunk), [5200, 130, 4444], [chunk, 1, chunk - 3], hq, hkv, d, dtype,
                  window, sinks)
+    out = run_prefill(p)
+    assert pk.get_error() == (0, 0)
+    assert_close(out, p)
+    assert torch.equal(out, run_prefill(p))
+
+
+@pytest.mark.parametrize("hq,hkv,d,dtype,chunk,window", [
+    (32, 8, 128, wl.BF16, 512, 1900), (24, 8, 64, wl.F16, 630, 1300), (32, 32, 128, wl.F16, 500, 700),
+    (32, 1, 128, wl.BF16, 473, 2 ** 31 - 1)])
+def test_prefill_window_items_of_one_query_tile(hq, hkv, d, dtype, chunk, window):
+    """Chunks of several query tiles, too few for two of them per work item."""
+    p = Windowed(wl.rng_for(chunk), [2100], [chunk], hq, hkv, d, dtype, window, 5)
     out = run_prefill(p)
     assert pk.get_error() == (0, 0)
     assert_close(out, p)

@@ -60,7 +60,8 @@ def test_workspace_sizes():
     assert size(1, 8, 8, 64, 4, 0) == 0 and size(1, 8, 8, 64, 4, 5, -1) == 0
     pre = pk.prefill_window_workspace_size
     assert pre(16, 8192, 512, 32, 8, 128, 1024, 4096) == 0        # enough work without a split
-    assert pre(1, 512, 512, 32, 8, 128, 1024, 4096) > 0
+    assert pre(1, 512, 512, 32, 8, 128, 1024, 4096) == 0          # as items of half the rows
+    assert pre(1, 256, 256, 32, 8, 128, 1024, 4096) > 0
     assert pre(1, 1, 512, 32, 8, 128, 1024, 4096) == pre(1, 1, 1, 32, 8, 128, 1024, 4096)
     assert pre(1, 5, 5, 6, 0, 64, 8, 5) == 0 and pre(1, 5, 5, 512, 1, 64, 8, 5) == 0
     with pytest.raises(ValueError):
