@@ -498,6 +498,8 @@ def rope_and_cache(q_out, q, k, v, key_cache, value_cache, slot_mapping, positio
     nb, hkv, bs, d = shape
     if value_cache.shape != shape:
         raise ValueError("key_cache and value_cache must match")
+    if q_out.dim() != 3 or q_out.shape[2] != d:
+        raise ValueError(f"q_out must be [T, Hq, {d}] of the cache dtype, got {list(q_out.shape)}")
     T, hq, _ = q_out.shape
     if slot_mapping.shape != (T,) or positions.shape != (rope.num_axes, T):
         raise ValueError(f"slot_mapping must be [{T}], positions [{rope.num_axes}, {T}]")
