@@ -302,7 +302,9 @@ int pa_decode_static_workspace(void *out, const void *q, const void *key_cache,
  * j < L when p - j < window or j < num_sinks; the sums of pa_decode run over
  * the tokens seen.  Only the table entries of blocks that hold such a token
  * are read; the others may hold anything (-1 after a trim).  Tokens not seen
- * may hold anything, NaN included, also inside a block that is read.
+ * may hold anything, NaN included, also inside a block that is read.  Among
+ * the tokens seen, one with a score of -infinity has weight 0 (a row of such
+ * tokens alone is zero), and a score of NaN or +infinity makes its row NaN.
  * window >= 1 (PA_ERR_INVALID_ARG otherwise; a window of 2^30 or more means
  * all), num_sinks >= 0, max_blocks_per_seq <= 2^26.  Everything else is as in
  * pa_decode / pa_decode_append, except that q and out must start on a 16-byte

@@ -675,6 +675,10 @@ __global__ void __launch_bounds__(NW * 32, NT == 1 ? PA_DECODE_MIN_CTAS : 3)
 constexpr int kMergeRows = 4;
 constexpr int kMergeFew = 8;  // rows of at most this many partitions load everything at once
 
+// A part of a row whose weights sum to l counts unless that is 0; a sum of NaN
+// (a NaN or +infinity among the scores) does, so that it reaches the row.
+__device__ __forceinline__ bool has_weight(float l) { return !(l <= 0.f); }
+
 template <typename T, int D>
 __device__ __forceinline__ void merge_row(const DecodeArgs &a, size_t row, int nparts, int lane) {
     const float2 *ml = a.ws_ml + row * a.num_parts;
@@ -690,10 +694,10 @@ __device__ __forceinline__ void merge_row(const DecodeArgs &a, size_t row, int n
 #pragma unroll
         for (int j = 0; j < kMergeFew; ++j)
             if (j < nparts && lane < D4) x[j] = op[(size_t)j * D4 + lane];
-        float M = v.y > 0.f ? v.x : -INFINITY;
+        float M = has_weight(v.y) ? v.x : -INFINITY;
 #pragma unroll
         for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
-        const float w = v.y > 0.f ? v.y * fast_exp2(v.x - M) : 0.f;
+        const float w = has_weight(v.y) ? v.y * fast_exp2(v.x - M) : 0.f;
 #pragma unroll
         for (int j = 0; j < kMergeFew; ++j) {
             const float wj = __shfl_sync(0xffffffffu, w, j);
@@ -702,7 +706,7 @@ __device__ __forceinline__ void merge_row(const DecodeArgs &a, size_t row, int n
                 acc.x += wj * x[j].x; acc.y += wj * x[j].y; acc.z += wj * x[j].z; acc.w += wj * x[j].w;
             }
         }
-        const float inv = den > 0.f ? 1.f / den : 0.f;
+        const float inv = has_weight(den) ? 1.f / den : 0.f;
         if (lane < D4) {
             uint16_t *out = reinterpret_cast<uint16_t *>(a.out) + row * D + 4 * lane;
             const uint32_t lo = (uint32_t)narrow1(acc.x * inv, T()) | ((uint32_t)narrow1(acc.y * inv, T()) << 16);
@@ -714,7 +718,7 @@ __device__ __forceinline__ void merge_row(const DecodeArgs &a, size_t row, int n
     float M = -INFINITY;
     for (int p = lane; p < nparts; p += 32) {
         const float2 v = ml[p];
-        if (v.y > 0.f) M = fmaxf(M, v.x);
+        if (has_weight(v.y)) M = fmaxf(M, v.x);
     }
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
@@ -723,7 +727,7 @@ __device__ __forceinline__ void merge_row(const DecodeArgs &a, size_t row, int n
         float w = 0.f;
         if (p < nparts) {
             const float2 v = ml[p];
-            w = v.y > 0.f ? v.y * fast_exp2(v.x - M) : 0.f;
+            w = has_weight(v.y) ? v.y * fast_exp2(v.x - M) : 0.f;
         }
         den += w;
         const int cnt = min(32, nparts - p0);
@@ -738,7 +742,7 @@ __device__ __forceinline__ void merge_row(const DecodeArgs &a, size_t row, int n
     }
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) den += __shfl_xor_sync(0xffffffffu, den, o);
-    const float inv = den > 0.f ? 1.f / den : 0.f;
+    const float inv = has_weight(den) ? 1.f / den : 0.f;
     if (lane < D4) {
         uint16_t *out = reinterpret_cast<uint16_t *>(a.out) + row * D + 4 * lane;
         const uint32_t lo = (uint32_t)narrow1(acc.x * inv, T()) | ((uint32_t)narrow1(acc.y * inv, T()) << 16);

@@ -395,8 +395,9 @@ __global__ void __launch_bounds__(NW * 32, U > 1 ? 1 : NT == 1 ? PA_DECODE_MIN_C
                     bm = fmaxf(bm, __shfl_xor_sync(0xffffffffu, bm, 8));
                     bm = fmaxf(bm, __shfl_xor_sync(0xffffffffu, bm, 16));
                     const float m_new = fmaxf(mrow[nt][j], bm);
-                    // a chunk's row may see nothing of the blocks so far
-                    const float m_ref = CHUNK && m_new == -INFINITY ? 0.f : m_new;
+                    // no score above -infinity so far (a visible key may give it,
+                    // and a chunk's row may see nothing of the blocks so far)
+                    const float m_ref = m_new == -INFINITY ? 0.f : m_new;
                     const float alpha = fast_exp2(mrow[nt][j] - m_ref);
                     float sum = 0.f;
 #pragma unroll
@@ -496,10 +497,10 @@ __global__ void __launch_bounds__(NW * 32, U > 1 ? 1 : NT == 1 ? PA_DECODE_MIN_C
         for (int e = lane; e < rows * D4; e += 32) {
             const int r = e / D4, d4 = e % D4;
             const float den = s_l[warp][r];
-            const float4 o = den > 0.f ? reinterpret_cast<const float4 *>(wacc)[e]
-                                       : make_float4(0.f, 0.f, 0.f, 0.f);
+            const float4 o = has_weight(den) ? reinterpret_cast<const float4 *>(wacc)[e]
+                                             : make_float4(0.f, 0.f, 0.f, 0.f);
             *reinterpret_cast<uint2 *>(out + q_row(r) * D + d4 * 4) =
-                narrow4(o, den > 0.f ? 1.f / den : 0.f, T());
+                narrow4(o, has_weight(den) ? 1.f / den : 0.f, T());
         }
         return;
     }
@@ -515,19 +516,19 @@ __global__ void __launch_bounds__(NW * 32, U > 1 ? 1 : NT == 1 ? PA_DECODE_MIN_C
         float M = -INFINITY;
 #pragma unroll
         for (int i = 0; i < NW; ++i)
-            if (s_l[i][r] > 0.f) M = fmaxf(M, s_m[i][r]);
+            if (has_weight(s_l[i][r])) M = fmaxf(M, s_m[i][r]);
         float den = 0.f;
         float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
         for (int i = 0; i < NW; ++i) {
-            if (s_l[i][r] > 0.f) {
+            if (has_weight(s_l[i][r])) {
                 const float wt = fast_exp2(s_m[i][r] - M);
                 const float4 x = reinterpret_cast<const float4 *>(rings + i * STAGES * Pipe::kStage)[e];
                 den += wt * s_l[i][r];
                 o.x += wt * x.x; o.y += wt * x.y; o.z += wt * x.z; o.w += wt * x.w;
             }
         }
-        const float inv = den > 0.f ? 1.f / den : 0.f;
+        const float inv = has_weight(den) ? 1.f / den : 0.f;
         if constexpr (CLUSTER) {
             // unnormalised, with the CTA's max and sum, to the CTA that joins it
             cluster_store4(cluster_addr(smem_addr(&r_o[part * slots + e % slots]), e / slots), o);
@@ -540,7 +541,7 @@ __global__ void __launch_bounds__(NW * 32, U > 1 ? 1 : NT == 1 ? PA_DECODE_MIN_C
                 o.x *= inv; o.y *= inv; o.z *= inv; o.w *= inv;
                 reinterpret_cast<float4 *>(a.ws_o)[(row * a.num_parts + part) * D4 + d4] = o;
                 if (d4 == 0)
-                    a.ws_ml[row * a.num_parts + part] = make_float2(den > 0.f ? M : -INFINITY, den);
+                    a.ws_ml[row * a.num_parts + part] = make_float2(has_weight(den) ? M : -INFINITY, den);
             }
         }
     }
@@ -557,12 +558,12 @@ __global__ void __launch_bounds__(NW * 32, U > 1 ? 1 : NT == 1 ? PA_DECODE_MIN_C
             for (int p = 0; p < ctas; ++p) {
                 const float2 ml = r_ml[p * RMAX + r];
                 const float4 x = r_o[p * slots + i];
-                const float wt = ml.y > 0.f ? fast_exp2(ml.x - M) : 0.f;
+                const float wt = has_weight(ml.y) ? fast_exp2(ml.x - M) : 0.f;
                 den += wt * ml.y;
                 o.x += wt * x.x; o.y += wt * x.y; o.z += wt * x.z; o.w += wt * x.w;
             }
             *reinterpret_cast<uint2 *>(out + q_row(r) * D + d4 * 4) =
-                narrow4(o, den > 0.f ? 1.f / den : 0.f, T());
+                narrow4(o, has_weight(den) ? 1.f / den : 0.f, T());
         }
     }
 }
@@ -590,14 +591,14 @@ __device__ __forceinline__ void merge_row_cta(const DecodeArgs &a, size_t row, i
     float M = -INFINITY, den = 0.f;
     for (int p = lane; p < nparts; p += 32) {
         const float2 v = ml[p];
-        if (v.y > 0.f) M = fmaxf(M, v.x);
+        if (has_weight(v.y)) M = fmaxf(M, v.x);
     }
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
     for (int p0 = 0; p0 < nparts; p0 += 32) {
         if (p0 > 0) load(p0);
         const float2 v = p0 + lane < nparts ? ml[p0 + lane] : make_float2(0.f, 0.f);
-        const float w = v.y > 0.f ? v.y * fast_exp2(v.x - M) : 0.f;
+        const float w = has_weight(v.y) ? v.y * fast_exp2(v.x - M) : 0.f;
         den += w;
 #pragma unroll
         for (int j = 0; j < PER; ++j) {
@@ -617,7 +618,7 @@ __device__ __forceinline__ void merge_row_cta(const DecodeArgs &a, size_t row, i
             const float4 y = s_acc[w][lane];
             acc.x += y.x; acc.y += y.y; acc.z += y.z; acc.w += y.w;
         }
-        const float inv = den > 0.f ? 1.f / den : 0.f;
+        const float inv = has_weight(den) ? 1.f / den : 0.f;
         uint16_t *out = reinterpret_cast<uint16_t *>(a.out) + row * D + 4 * lane;
         const uint32_t lo = (uint32_t)narrow1(acc.x * inv, T()) | ((uint32_t)narrow1(acc.y * inv, T()) << 16);
         const uint32_t hi = (uint32_t)narrow1(acc.z * inv, T()) | ((uint32_t)narrow1(acc.w * inv, T()) << 16);
