@@ -336,9 +336,10 @@ size_t pa_decode_window_workspace_size(int32_t num_seqs, int32_t num_q_heads, in
  * Query row i of sequence s sits at position p = L - n_s + i, as in
  * pa_prefill, and sees token j when j <= p and (p - j < window or
  * j < num_sinks).  Table entries of blocks that no row of the chunk sees are
- * not read.  Tokens that no row of the chunk sees may hold anything; a token
- * that some row sees must be finite, since rows that do not see it still
- * multiply its value by a zero weight.
+ * not read.  Tokens that no row of the chunk sees may hold anything; one that
+ * some row sees must have a finite value, since rows that do not see it still
+ * multiply that by a zero weight.  Scores that are not finite: as in
+ * pa_decode_window.
  *
  * Short chunks run on the decode kernel, up to 16 query rows at a time, longer
  * ones on the tcgen05 kernel, whichever the sizes make faster (at most 8 query

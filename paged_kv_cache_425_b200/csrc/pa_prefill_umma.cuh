@@ -62,6 +62,8 @@
 // and the tensor memory is released before the CTA exits.
 #pragma once
 
+#include <cfloat>
+
 #include "pa_exp2.cuh"
 #include "pa_kernels.cuh"
 #include "pa_umma.cuh"
@@ -527,7 +529,9 @@ __global__ void __launch_bounds__(kUmmaThreads, 1)
             const int qi = rvalid ? R / G : 0, qh = rvalid ? R % G : 0;
             const int pos = rvalid ? it.L - it.n + qi : it.nkeys - 1;  // last key this row sees
             const int live_end = min(it.L, it.nblk * kBlock);  // keys from here on hold no data
-            float m_run = kMaskedLogit, l = 0.f;
+            // (WIN: under every finite score; masked ones are -infinity)
+            constexpr float kNoScore = WIN ? -FLT_MAX : kMaskedLogit;
+            float m_run = kNoScore, l = 0.f;
             const int j0 = one ? k : 0, dj = one ? 2 : 1;  // key tiles of this warpgroup
             for (int j = j0; j < it.ntiles; j += dj) {
                 const int g = gt + j;
@@ -580,7 +584,7 @@ __global__ void __launch_bounds__(kUmmaThreads, 1)
                 }
                 // the max of the raw scores (scale > 0 keeps the order); three-input
                 // max, four independent chains
-                float mx4[4] = {kMaskedLogit, kMaskedLogit, kMaskedLogit, kMaskedLogit};
+                float mx4[4] = {kNoScore, kNoScore, kNoScore, kNoScore};
                 if constexpr (WIN) {
                     // -infinity: a row may see nothing of its first tiles
                     if (vis_b > vis_a || vis_end < kUmmaKeys || bad) {
@@ -700,6 +704,10 @@ __global__ void __launch_bounds__(kUmmaThreads, 1)
             }
             tc_fence_after();
             if constexpr (WIN) {
+                // The row's maximum has the weight 1 (within 8e-5), so a smaller
+                // sum is of clamped weights alone (exp2_fma_pair makes 2^-125 of
+                // -infinity): the row has seen nothing.  NaN stays.
+                l = l < 0.5f ? 0.f : l;
                 if (one) {
                     if (k == 1) {  // hand (max, sum) over, and O_1 where it is
                         s_half[r] = make_float2(m_run, l);
@@ -748,7 +756,7 @@ __global__ void __launch_bounds__(kUmmaThreads, 1)
                     ++halves;
                 }
             }
-            const float inv = l > 0.f ? 1.f / l : 0.f;
+            const float inv = has_weight(l) ? 1.f / l : 0.f;
             if constexpr (WIN) {
                 if (it.nparts > 1) {  // one of several splits: its share to the workspace
                     const size_t slot = ((umma_item_index(a, it.s, it.tile, it.kvh) * pw.splits + it.part) *
@@ -860,7 +868,7 @@ __global__ void __launch_bounds__(kUmmaRows)
         }
         float m = M;
 #pragma unroll
-        for (int q = 0; q < P; ++q) m = fmaxf(m, v[q].y > 0.f ? v[q].x : -INFINITY);
+        for (int q = 0; q < P; ++q) m = fmaxf(m, has_weight(v[q].y) ? v[q].x : -INFINITY);
         const float old = m == -INFINITY ? 0.f : fast_exp2(M - m);
         M = m;
         den *= old;
@@ -870,7 +878,7 @@ __global__ void __launch_bounds__(kUmmaRows)
         }
 #pragma unroll
         for (int q = 0; q < P; ++q) {
-            const float wt = p0 + q < nparts && v[q].y > 0.f ? fast_exp2(v[q].x - M) : 0.f;
+            const float wt = p0 + q < nparts && has_weight(v[q].y) ? fast_exp2(v[q].x - M) : 0.f;
             den += wt * v[q].y;
 #pragma unroll
             for (int u = 0; u < V; ++u) {
@@ -879,7 +887,7 @@ __global__ void __launch_bounds__(kUmmaRows)
             }
         }
     }
-    const float inv = den > 0.f ? 1.f / den : 0.f;
+    const float inv = has_weight(den) ? 1.f / den : 0.f;
     uint16_t *out = reinterpret_cast<uint16_t *>(a.out) +
                     ((size_t)(w.q0 + R / G) * a.num_q_heads + (size_t)kvh * G + R % G) * D + c0 * 4;
 #pragma unroll

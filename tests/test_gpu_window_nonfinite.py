@@ -5,7 +5,7 @@ import numpy as np
 import pytest
 
 import window_shapes as ws
-from test_gpu_window import run_decode
+from test_gpu_window import run_decode, run_prefill
 
 torch = pytest.importorskip("torch")
 pytestmark = pytest.mark.gpu
@@ -23,4 +23,15 @@ def test_decode_window(shape, kind, heads):
     ws.not_finite(p, kind)
     out, live = run_decode(p)
     assert bool(live.all())
+    assert ws.worst(gh.to_f64(out), p) <= 1.0
+
+
+@pytest.mark.parametrize("kind", ws.KINDS)
+@pytest.mark.parametrize("shape", ws.PREFILL)
+def test_prefill_window(shape, kind):
+    """150 sinks: whole key tiles of -infinity in front of the window."""
+    p = ws.prefill_problem(shape, 150 if kind in ("half", "all") else 1)
+    ws.not_finite(p, kind)
+    out = run_prefill(p)
+    assert pk.get_error() == (0, 0)
     assert ws.worst(gh.to_f64(out), p) <= 1.0
