@@ -309,7 +309,8 @@ int pa_decode_static_workspace(void *out, const void *q, const void *key_cache,
  * all), num_sinks >= 0, max_blocks_per_seq <= 2^26.  Everything else is as in
  * pa_decode / pa_decode_append, except that q and out must start on a 16-byte
  * boundary and that the workspace's size comes from
- * pa_decode_window_workspace_size for the same arguments (0: may be NULL).
+ * pa_decode_window_workspace_size for the same arguments (0: may be NULL) and
+ * the same current device: the split depends on what the device holds at once.
  * A row's partitions are joined in a fixed order: equal calls give equal bits.
  */
 int pa_decode_window(void *out, const void *q, const void *key_cache, const void *value_cache,
@@ -346,10 +347,11 @@ size_t pa_decode_window_workspace_size(int32_t num_seqs, int32_t num_q_heads, in
  * rows per kv head always on the first, groups above 16 always on the second;
  * pa_prefill_select does not matter here).  Either splits a row's keys when
  * there is too little work for the GPU; the parts go to `workspace`
- * (pa_prefill_window_workspace_size bytes for the same arguments, 256-byte
- * aligned; may be NULL when that is 0) and are joined in a fixed order.  The
- * size does not grow with every argument: a smaller batch may be split where a
- * larger one is not.  Calls that share a workspace must not overlap.
+ * (pa_prefill_window_workspace_size bytes for the same arguments and current
+ * device, 256-byte aligned; may be NULL when that is 0) and are joined in a
+ * fixed order.  The size does not grow with every argument: a smaller batch may
+ * be split where a larger one is not.  Calls that share a workspace must not
+ * overlap.
  *
  * window and num_sinks as in pa_decode_window.  q and out start on 16-byte
  * boundaries.  PA_ERR_UNSUPPORTED for scale <= 0 or not finite, and for more

@@ -18,6 +18,7 @@
 #include "pa_prefill_umma.cuh"
 #include "pa_rope.cuh"
 #include "pa_window.cuh"
+#include "pa_window_plan.cuh"
 
 namespace pa {
 namespace {
@@ -769,163 +770,59 @@ int pa_version(void) { return 100; }
 namespace pa {
 namespace {
 
-// Positions stay below 2^30 (the table's width is checked), so a longer
-// window or sink run means "all" and is cut to that.
-constexpr int32_t kWindowMax = 1 << 30;
-
-// Most blocks a call may have to read for one run of `queries` consecutive
-// query tokens: the sinks' and those any placement of the window touches.
-int64_t window_visible_blocks(int32_t max_blocks_per_seq, int32_t queries, int32_t window,
-                              int32_t num_sinks) {
-    const int64_t w = ((int64_t)window + queries - 1 + 2 * (kBlock - 1)) / kBlock;
-    const int64_t k = ((int64_t)num_sinks + kBlock - 1) / kBlock;
-    return std::min<int64_t>(max_blocks_per_seq, w + k);
-}
-
-// How a windowed call runs: on decode_window_kernel (runs of tile_tokens query
-// tokens; few rows: `cluster` CTAs each, many: `parts` partitions each), or on
-// prefill_umma_kernel (umma; `parts` ranges of split_tiles key tiles).
-struct WindowPlan {
-    bool umma;
-    bool warp_runs;
-    int tile_tokens, cluster, part_blocks, qtiles, split_tiles;
-    int64_t parts;
-    // rows of the workspace, each with `parts` partial results
-    int64_t ws_rows;
-};
-
-constexpr int kWindowSms = 148;
-constexpr int kChunkRows = 16;  // rows of a run on decode_window_kernel
-// Shapes of decode_window_kernel (see there): warps per CTA and blocks in
-// flight per warp.  Few rows at head_dim 128: 6 warps x 4 blocks, up to 8 %
-// faster than 8 x 3; at 64: 8 x 6, 6 % faster than 6 x 8.  A lane holds one
-// block id, so a CTA takes 32 blocks per warp at most.
-template <int D>
-constexpr int kFewWarps = D == 128 ? 6 : 8;
-template <int D>
-constexpr int kFewStages = D == 128 ? 4 : 6;
-constexpr int kMinFewWarps = 6, kManyWarps = 4, kManyStages = 3;
-constexpr int kWarpRunBlocks = 6;
-constexpr int kFewBlocks = 32 * kMinFewWarps, kManyBlocks = 32 * kManyWarps;
-
-// The heads, window and widths were checked: 1 <= group <= kUmmaRows.
-WindowPlan window_plan(int64_t num_seqs, int32_t num_q_tokens, int32_t max_query_len,
-                       int32_t num_q_heads, int32_t num_kv_heads, int32_t max_blocks_per_seq,
-                       int32_t window, int32_t num_sinks) {
-    const int group = num_q_heads / num_kv_heads;
-    WindowPlan p = {};
-    p.ws_rows = (int64_t)num_q_tokens * num_q_heads;
-    // decode_window_kernel: runs of at most kChunkRows rows
-    const int64_t run_tokens =
-        max_query_len * (int64_t)group <= 8 ? max_query_len : std::max(kChunkRows / group, 1);
-    const int64_t runs = num_seqs * num_kv_heads * ((max_query_len + run_tokens - 1) / run_tokens);
-    const int64_t blocks =
-        window_visible_blocks(max_blocks_per_seq, (int32_t)run_tokens, window, num_sinks);
-    // prefill_umma_kernel: items of two query tiles (halved below where that is
-    // faster), walked in tiles of 128 keys
-    constexpr int kTileBlocks = kUmmaKeys / kBlock;
-    const int64_t item_tokens = kUmmaQTiles * (kUmmaRows / group);
-    const int64_t items = num_seqs * num_kv_heads * ((max_query_len + item_tokens - 1) / item_tokens);
-    const int64_t tiles =
-        (window_visible_blocks(max_blocks_per_seq, (int32_t)std::min<int64_t>(max_query_len, item_tokens),
-                               window, num_sinks) + kTileBlocks - 1) / kTileBlocks;
-    // one query tile per item: both warpgroups share its key tiles
-    const bool one = max_query_len <= kUmmaRows / group;
-    // Few rows keep most of a 256-row item empty.  The decode kernel takes about
-    // 1.5 ns per (run, block) while the GPU holds the runs at once, the other
-    // about 2.1 us per key tile on each of the 148 SMs (half for one query tile)
-    // and 6 us more at its ends.  Of 90 measured shapes this takes the faster
-    // one or one at most 20 % slower (40 tokens, window 100: 6.3 us here, 10.3
-    // there; 32 tokens of 4 heads, window 4096: 25.5 us here, 17.6 there).
-    // Beyond one wave of runs only those of few blocks (a warp each) may stay
-    // there: 4 + 0.9 ns per block a run against 5 or 7 us an item and its tiles (31
-    // x 32 heads x 48 tokens: 21 us here, 43 there).
-    const bool wave = runs <= kWindowSms * PA_DECODE_MIN_CTAS;
-    const bool warp_runs = !wave && blocks <= kWarpRunBlocks;
-    const double rounds = (double)((items + kWindowSms - 1) / kWindowSms);
-    const bool slower =
-        wave ? 2 * runs * blocks > 8400 + (one ? 11 : 22) * items * tiles
-             : !warp_runs || 1e-3 * runs * (4 + 0.9 * blocks) >
-                                 rounds * (one ? 5 + 0.9 * tiles : 7 + 2.1 * tiles);
-    p.umma = group > kChunkRows ||
-             (max_query_len > 1 && (int64_t)max_query_len * group > 8 && slower);
-    if (p.umma) {
-        // Query tiles and key ranges per item: the fewest microseconds over the
-        // rounds that 148 CTAs need (2.1 per key tile, half for one query tile, and
-        // 3 per item), plus the launch of the join and its traffic.  Measured: 8
-        // items of 33 tiles 70 us unsplit, 43 in 2 ranges, 28 in 4, 20.3 in 11, 23
-        // in 17; 64 items of 33 tiles 72 us, 51 in 2 ranges, 47 as 128 of one
-        // query tile.
-        double best = 0;
-        for (int qtiles = kUmmaQTiles; qtiles >= 1; --qtiles) {
-            const int64_t tokens = qtiles * (kUmmaRows / group);
-            const int64_t count =
-                num_seqs * num_kv_heads * ((max_query_len + tokens - 1) / tokens);
-            const int64_t t = (window_visible_blocks(max_blocks_per_seq,
-                                                     (int32_t)std::min<int64_t>(max_query_len, tokens),
-                                                     window, num_sinks) + kTileBlocks - 1) / kTileBlocks;
-            const bool single = one || qtiles == 1;
-            const double per_tile = single ? 1.05 : 2.1, per_range = single ? 0.03 : 0.06;
-            for (int64_t n = 1; n <= 64 && n <= t; ++n) {
-                const int64_t per = (t + n - 1) / n, used = (t + per - 1) / per;
-                const double cost =
-                    (double)((count * used + kWindowSms - 1) / kWindowSms) * (per_tile * per + 3.0) +
-                    (used > 1 ? 3.0 + per_range * count * used + 0.25 * used : 0.0);
-                if (p.parts == 0 || cost < best) {
-                    best = cost;
-                    p.qtiles = qtiles;
-                    p.tile_tokens = (int)tokens;
-                    p.parts = used;
-                    p.split_tiles = (int)per;
-                    p.ws_rows = count * kUmmaQTiles * kUmmaRows;
-                }
-            }
-            if (one) break;  // a second query tile would be empty either way
-        }
-        return p;
+// Room for clusters of the few-rows shape on the current device, looked up
+// once per device and CUDA context (every build of it takes an SM per CTA).
+// The size queries ask as the calls do, so both make the same plan.
+WindowDevice window_device() {
+    struct Entry {
+        int dev;
+        unsigned long long ctx;
+        WindowDevice room;
+    };
+    static std::mutex mu;
+    static std::vector<Entry> seen;
+    int dev = -1;
+    if (cudaGetDevice(&dev) != cudaSuccess) {
+        cudaGetLastError();
+        return kMeasuredDevice;
     }
-    p.tile_tokens = (int)run_tokens;
-    p.parts = 1;
-    if (runs <= kWindowSms && blocks > kManyWarps) {
-        // A cluster as large as finds room for every run at once, while each
-        // warp keeps a block.  At one CTA per SM the GPU holds so many clusters
-        // of that size (its CTAs need SMs of one partition of the GPU; sizes
-        // that hold no more than the next larger one are left out); a second
-        // wave doubles the time.
-        constexpr struct {
-            int ctas, room;
-        } kClusters[] = {{16, 7}, {10, 11}, {9, 15}, {6, 22}, {5, 26}, {4, 33}, {3, 45}, {2, 74}, {1, kWindowSms}};
-        int ctas = 1;
-        for (const auto &c : kClusters)
-            if (runs <= c.room) {
-                ctas = (int)std::min<int64_t>(c.ctas, (blocks + kMinFewWarps - 1) / kMinFewWarps);
-                break;
-            }
-        // (up to three blocks per warp the next shape's one CTA is done before a
-        // cluster has joined its sums: 9 blocks 3.0 us, 3.7 in a cluster of two;
-        // 20 blocks 5.3 and 4.5)
-        if ((blocks + ctas - 1) / ctas <= kFewBlocks && (ctas == 1 || blocks > 3 * kManyWarps)) {
-            p.cluster = ctas;
-            return p;
-        }
+    unsigned long long ctx = current_context_id();
+    {
+        std::lock_guard<std::mutex> lock(mu);
+        for (const Entry &e : seen)
+            if (ctx != 0 && e.dev == dev && e.ctx == ctx) return e.room;
     }
-    if (runs <= 2 * kWindowSms && blocks > kManyWarps && blocks <= kManyBlocks) {
-        p.part_blocks = 0;  // one CTA per run, all at once (256 runs of 64 blocks: 24.3 us, split 28.5)
-        return p;
+    constexpr int D = 128, NW = kFewWarps<D>, ST = kFewStages<D>, SMEM = NW * ST * WarpPipe<D, ST>::kStage + 1024;
+    static_assert(2 * SMEM > 227 * 1024, "an SM per CTA");
+    auto k = decode_window_kernel<__nv_bfloat16, D, NW, ST, 2, 0, 1, false, true, false>;
+    Entry e = {dev, 0, {}};
+    const bool wide = set_smem(k, SMEM) && allow_cluster16(k);
+    for (int c = 1; wide && c <= kMaxCluster; ++c) {
+        cudaLaunchConfig_t cfg = {};
+        cfg.gridDim = dim3(1, c, 1);
+        cfg.blockDim = dim3(NW * 32);
+        cfg.dynamicSmemBytes = SMEM;
+        cudaLaunchAttribute attr;
+        attr.id = cudaLaunchAttributeClusterDimension;
+        attr.val.clusterDim.x = 1;
+        attr.val.clusterDim.y = c;
+        attr.val.clusterDim.z = 1;
+        cfg.attrs = &attr;
+        cfg.numAttrs = 1;
+        int n = 0;
+        if (cudaOccupancyMaxActiveClusters(&n, k, &cfg) == cudaSuccess)
+            e.room.room[c] = n;
+        else
+            cudaGetLastError();  // a size this GPU launches none of is not the caller's error
     }
-    // more runs than a wave of CTAs holds, of a few blocks each (7360 runs: 1 block
-    // 18 us, 40 as a CTA per run; 2 blocks 26 and 42, 6 blocks 57 and 65, 8 blocks
-    // 84 and 74)
-    if (warp_runs) {
-        p.warp_runs = true;
-        return p;
+    if (!wide) cudaGetLastError();
+    if (e.room.room[1] <= 0) return kMeasuredDevice;
+    e.ctx = current_context_id();  // the lookup may have made the context
+    if (e.ctx != 0) {
+        std::lock_guard<std::mutex> lock(mu);
+        seen.push_back(e);
     }
-    // 512-token partitions, or 1024 where that still makes several of a run
-    // (1024 runs of 258 blocks: 314 us, 325 with the shorter ones; 384 runs of
-    // up to 131: 63.3 and 61.7)
-    p.part_blocks = blocks >= 8 * kPartBlocks ? 2 * kPartBlocks : kPartBlocks;
-    p.parts = (blocks + p.part_blocks - 1) / p.part_blocks;
-    return p;
+    return e.room;
 }
 
 template <typename T, int D, int NW, int ST, int U, int PB, int NT, bool CHUNK, bool CLUSTER, bool WARP = false>
@@ -1054,7 +951,7 @@ int decode_window_call(void *out, const void *q, const void *k_new, const void *
         return PA_ERR_INVALID_ARG;
     window = std::min(window, kWindowMax);
     num_sinks = std::min(num_sinks, kWindowMax);
-    const WindowPlan plan = window_plan(num_seqs, num_seqs, 1, num_q_heads, num_kv_heads, max_blocks_per_seq,
+    const WindowPlan plan = window_plan(window_device(), num_seqs, num_seqs, 1, num_q_heads, num_kv_heads, max_blocks_per_seq,
                                         window, num_sinks);
     WindowArgs a = {};
     a.d.out = out;
@@ -1098,7 +995,7 @@ size_t pa_decode_window_workspace_size(int32_t num_seqs, int32_t num_q_heads, in
         head_dim <= 0 || block_size != kBlock || max_blocks_per_seq <= 0 ||
         check_window(window, num_sinks, max_blocks_per_seq) != PA_OK)
         return 0;
-    return window_workspace(window_plan(num_seqs, num_seqs, 1, num_q_heads, num_kv_heads,
+    return window_workspace(window_plan(window_device(), num_seqs, num_seqs, 1, num_q_heads, num_kv_heads,
                                         max_blocks_per_seq, window, num_sinks),
                             head_dim);
 }
@@ -1140,7 +1037,7 @@ size_t pa_prefill_window_workspace_size(int32_t num_seqs, int32_t num_q_tokens,
         check_window(window, num_sinks, max_blocks_per_seq) != PA_OK)
         return 0;
     max_query_len = std::min(max_query_len, num_q_tokens);
-    return window_workspace(window_plan(num_seqs, num_q_tokens, max_query_len, num_q_heads,
+    return window_workspace(window_plan(window_device(), num_seqs, num_q_tokens, max_query_len, num_q_heads,
                                         num_kv_heads, max_blocks_per_seq, window, num_sinks),
                             head_dim);
 }
@@ -1176,7 +1073,7 @@ int pa_prefill_window(void *out, const void *q, const void *key_cache, const voi
     window = std::min(window, kWindowMax);
     num_sinks = std::min(num_sinks, kWindowMax);
 
-    const WindowPlan plan = window_plan(num_seqs, num_q_tokens, max_query_len, num_q_heads, num_kv_heads,
+    const WindowPlan plan = window_plan(window_device(), num_seqs, num_q_tokens, max_query_len, num_q_heads, num_kv_heads,
                                         max_blocks_per_seq, window, num_sinks);
     if (plan.parts > 65535) return PA_ERR_UNSUPPORTED;
     WindowArgs a = {};
