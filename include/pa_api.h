@@ -409,6 +409,7 @@ int pa_window_call(const pa_window_args *args);
  */
 #define PA_ROPE_MAX_PAIRS 64
 #define PA_ROPE_MAX_AXES 8
+#define PA_ROPE_MAX_INV_FREQ 128.0f
 typedef struct {
     uint64_t turns[PA_ROPE_MAX_PAIRS]; /* inv_freq / (2 pi) modulo 1, times 2^64 */
     uint8_t axis[PA_ROPE_MAX_PAIRS];
@@ -417,8 +418,8 @@ typedef struct {
 
 /* Fill *rope.  inv_freq: host, [num_pairs], finite; pair_axes: host,
  * [num_pairs], values in [0, num_axes), or NULL for axis 0 everywhere.
- * num_pairs is a multiple of 8 up to 64, num_axes at most 8
- * (PA_ERR_UNSUPPORTED otherwise).  On an error *rope is left as it was. */
+ * num_pairs is a multiple of 8 up to 64, num_axes at most 8, |inv_freq| at most
+ * PA_ROPE_MAX_INV_FREQ (PA_ERR_UNSUPPORTED otherwise).  On an error *rope is left as it was. */
 int pa_rope_init(pa_rope *rope, const float *inv_freq, const int32_t *pair_axes, int32_t num_pairs,
                  int32_t num_axes, int32_t interleaved);
 
@@ -430,8 +431,9 @@ int pa_rope_init(pa_rope *rope, const float *inv_freq, const int32_t *pair_axes,
  * slot = slot_mapping[t] >= 0 the turned k[t][g] and v[t][g] (as it is) go to
  * that slot for every kv head, as in pa_reshape_and_cache (negative: padding;
  * beyond the pool: skipped, PA_DEVERR_SLOT; two tokens with one slot race).
- * The angle is exact modulo a turn for every int32 position; cos and sin are
- * taken in f32, the products summed in f32 and rounded once to dtype.
+ * For every int32 position the angle, modulo a turn, is within
+ * 2^-32 + |inv_freq| 2^-34 of a turn of the exact one; cos and sin are taken in
+ * f32, the products summed in f32 and rounded once to dtype.
  *
  *   q, k, v       device, dtype; token t's heads start at t * stride elements
  *                 (strides >= 0 and multiples of 8, so the three may be slices

@@ -448,7 +448,7 @@ class Rope:
     """Rotary positions of a model: pair i of a head turns by
     positions[pair_axes[i]] * inv_freq[i].
 
-    inv_freq: [pairs] (used as float32); pair_axes: [pairs] axis numbers, or
+    inv_freq: [pairs] (used as float32, at most 128 in size); pair_axes: [pairs] axis numbers, or
     None for a single axis; interleaved: pairs are (2i, 2i + 1) instead of
     (i, i + pairs); num_axes: rows of the positions tensor (default: the
     largest axis used, plus one)."""

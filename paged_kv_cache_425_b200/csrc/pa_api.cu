@@ -1135,8 +1135,12 @@ int pa_rope_init(pa_rope *rope, const float *inv_freq, const int32_t *pair_axes,
     for (int32_t i = 0; i < num_pairs; ++i) {
         const int32_t axis = pair_axes ? pair_axes[i] : 0;
         if (axis < 0 || axis >= num_axes || !std::isfinite(inv_freq[i])) return PA_ERR_INVALID_ARG;
-        // the angle of one position step in turns, modulo a whole turn, as a
-        // 64-bit fraction: long double keeps 64 bits of the quotient
+        if (std::fabs(inv_freq[i]) > PA_ROPE_MAX_INV_FREQ) return PA_ERR_UNSUPPORTED;
+        // The angle of one position step in turns, modulo a whole turn, as a
+        // 64-bit fraction.  long double keeps 64 bits of the quotient, those of
+        // its whole turns among them: with 2 pi and the division rounded it is
+        // off by less than 2^-63 |turns|, the difference and the cut to 64 bits
+        // by less than 2^-63.4 more, and a position multiplies that by up to 2^31.
         const long double turns = (long double)inv_freq[i] / 6.28318530717958647692528676655900577L;
         long double frac = turns - std::floor(turns);
         r.turns[i] = frac >= 1.0L ? 0 : (uint64_t)(frac * 18446744073709551616.0L);

@@ -6,8 +6,9 @@
 // The angle is held as a 64-bit fraction of a turn: the position times the
 // fraction of one step (pa_rope_init), modulo 2^64.  The multiplication wraps
 // exactly where whole turns drop out, so a far position needs no range
-// reduction and loses nothing; cos and sin come from cospif / sinpif of the
-// top 32 bits, in f32, and each output is rounded once.
+// reduction and adds only the step's own rounding (under 2^-63 of a turn, 2^-32
+// at position 2^31, for frequencies up to 1); cos and sin come from sincospif
+// of the top 32 bits, in f32, and each output is rounded once.
 //
 // Memory bound (every q, k, v element is read once and written once; the
 // angles are shared by all heads of a token).  One CTA per token: its threads

@@ -1,5 +1,8 @@
 """Calls of the windowed and rotary binding that are refused on the host, before
-any address reaches the library (no GPU needed)."""
+any address reaches the library, and the limits of those that are not (no GPU
+needed)."""
+from fractions import Fraction
+
 import numpy as np
 import pytest
 
@@ -18,3 +21,39 @@ def test_rope_refuses_a_q_out_of_another_head_dim(shape):
     with pytest.raises(ValueError, match="q_out must be"):
         pk.rope_and_cache(torch.zeros(shape, dtype=torch.float16), q, k, k, cache, cache.clone(),
                           torch.zeros(3, dtype=torch.int64), torch.zeros(1, 3, dtype=torch.int32), rope)
+
+
+def inverse_turn(bits):
+    """1 / (2 pi) within 2^-bits: pi by Machin's formula in exact arithmetic."""
+    def arctan_of_inverse(n):
+        total, k, term = 0, 0, (1 << (bits + 16)) // n
+        while term:
+            total += (-1) ** k * (term // (2 * k + 1))
+            term //= n * n
+            k += 1
+        return total
+    pi = 4 * (4 * arctan_of_inverse(5) - arctan_of_inverse(239))
+    return Fraction(1 << (bits + 16), 2 * pi)
+
+
+def test_rope_angles_keep_their_bound():
+    """Position times the stored step against exact arithmetic: at most
+    2^-32 + |inv_freq| 2^-34 of a turn for every int32 position."""
+    inv = inverse_turn(160)
+    rng = np.random.default_rng(5)
+    freq = np.concatenate([np.exp(rng.uniform(np.log(1e-9), np.log(128), size=46)) * rng.choice([-1, 1], size=46),
+                           [128, -128, 127.99999, 1, -1, 2.0 ** -149, -2.0 ** -149, 0.0, -1e-30, 6.2831855]])
+    freq = freq.astype(np.float32)
+    rope = pk.Rope(np.concatenate([freq, np.zeros(-len(freq) % 8, np.float32)]))
+    for f, step in zip(freq, rope._struct.turns):
+        for p in (1, -1, 12345, 2 ** 31 - 1, -2 ** 31):
+            d = (Fraction(p * step, 2 ** 64) - p * Fraction(float(f)) * inv) % 1
+            assert min(d, 1 - d) <= Fraction(1, 2 ** 32) + abs(Fraction(float(f))) / 2 ** 34
+
+
+@pytest.mark.parametrize("f", [128.00002, -129.0, 1e6, -1e12, 3e38])
+def test_rope_refuses_frequencies_beyond_its_bound(f):
+    """A step that cannot be held closely enough turned far tokens by anything."""
+    with pytest.raises(pk.PagedError) as e:
+        pk.Rope(np.array([1.0] * 7 + [f], np.float32))
+    assert e.value.status == pk.PA_ERR_UNSUPPORTED
