@@ -306,9 +306,10 @@ int pa_decode_static_workspace(void *out, const void *q, const void *key_cache,
  * the tokens seen, one with a score of -infinity has weight 0 (a row of such
  * tokens alone is zero), and a score of NaN or +infinity makes its row NaN.
  * window >= 1 (PA_ERR_INVALID_ARG otherwise; a window of 2^30 or more means
- * all), num_sinks >= 0, max_blocks_per_seq <= 2^26.  Everything else is as in
- * pa_decode / pa_decode_append, except that q and out must start on a 16-byte
- * boundary and that the workspace's size comes from
+ * all), num_sinks >= 0, max_blocks_per_seq <= 2^26 (PA_ERR_UNSUPPORTED above,
+ * and where more than 65535 partitions of 1024 tokens are visible).  Everything
+ * else is as in pa_decode / pa_decode_append, except that q and out must start
+ * on a 16-byte boundary and that the workspace's size comes from
  * pa_decode_window_workspace_size for the same arguments (0: may be NULL) and
  * the same current device: the split depends on what the device holds at once.
  * A row's partitions are joined in a fixed order: equal calls give equal bits.

@@ -942,7 +942,8 @@ int decode_window_call(void *out, const void *q, const void *k_new, const void *
     bool empty = false;
     int rc = check_decode_args(out, q, key_cache, value_cache, block_tables, context_lens,
                                num_kv_heads, num_seqs, num_q_heads, head_dim, block_size,
-                               max_blocks_per_seq, num_blocks, dtype, &empty);
+                               // (its limit on partitions is the whole table's)
+                               std::min(max_blocks_per_seq, 1), num_blocks, dtype, &empty);
     if (rc != PA_OK) return rc;
     rc = check_window(window, num_sinks, max_blocks_per_seq);
     if (rc != PA_OK || empty) return rc;

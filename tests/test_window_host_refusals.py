@@ -57,3 +57,18 @@ def test_rope_refuses_frequencies_beyond_its_bound(f):
     with pytest.raises(pk.PagedError) as e:
         pk.Rope(np.array([1.0] * 7 + [f], np.float32))
     assert e.value.status == pk.PA_ERR_UNSUPPORTED
+
+
+def test_decode_window_takes_tables_as_wide_as_documented():
+    """2^26 blocks per sequence: the refusals that follow the width's check are
+    reached (nothing is launched)."""
+    import ctypes
+    p = ctypes.c_void_p(4096)  # aligned, never dereferenced
+
+    def call(width, window, ws=None):
+        tail = (p, p, window, 4, 2, 0.1, 100, 8, 64, 16, width, 100, 0, ws, 0, None)
+        return (pk.pa_decode_window(p, p, p, p, *tail), pk.pa_decode_append_window(p, p, None, p, p, p, *tail))
+    assert call(1 << 26, 5000) == (pk.PA_ERR_WORKSPACE, pk.PA_ERR_INVALID_ARG)
+    assert call((1 << 26) + 1, 5000) == (pk.PA_ERR_UNSUPPORTED,) * 2
+    # more than 65535 partitions: the part of pa_decode_window that stays refused
+    assert call(1 << 26, 2 ** 31 - 1)[0] == pk.PA_ERR_UNSUPPORTED
