@@ -665,7 +665,8 @@ class BlockAllocator:
     def trim_window(self, seq_id: int, next_position: int, window: int, num_sinks: int = 0) -> int:
         """Drop the blocks no query at next_position or later can see; returns
         how many.  Their table entries become -1."""
-        n = pa_alloc_trim_window(self._h, seq_id, next_position, window, num_sinks)
+        n = pa_alloc_trim_window(self._h, seq_id, _i32_arg(next_position, "next_position"),
+                                 _i32_arg(window, "window"), _i32_arg(num_sinks, "num_sinks"))
         _check(min(n, 0), "pa_alloc_trim_window")
         return n
 

@@ -72,3 +72,13 @@ def test_decode_window_takes_tables_as_wide_as_documented():
     assert call((1 << 26) + 1, 5000) == (pk.PA_ERR_UNSUPPORTED,) * 2
     # more than 65535 partitions: the part of pa_decode_window that stays refused
     assert call(1 << 26, 2 ** 31 - 1)[0] == pk.PA_ERR_UNSUPPORTED
+
+
+@pytest.mark.parametrize("args", [(64, 2 ** 32 + 16, 0), (64, 16, 2 ** 32), (2 ** 32 + 64, 16, 0), (64, 2 ** 63, 0)])
+def test_trim_refuses_arguments_that_do_not_fit_32_bits(args):
+    """Cut to 32 bits, a window of 2^32 + 16 would free blocks that are in sight."""
+    a = pk.BlockAllocator(8)
+    a.add_seq(1, 64)
+    with pytest.raises(ValueError, match="32 bits"):
+        a.trim_window(1, *args)
+    assert (a.block_table(1) >= 0).all() and a.stats()["used_blocks"] == 4
