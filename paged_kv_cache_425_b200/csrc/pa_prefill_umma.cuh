@@ -52,9 +52,10 @@
 // other key tile instead: S_k, P_k and O_k are then those of key tiles
 // k, k + 2, ... and warpgroup 0 joins the two halves at the end, reading O_1
 // from tensor memory.  Measured (bf16, 32 heads on 8, head_dim 128, 4096-token
-// windows): 16 chunks of 512 tokens 515 us, 1.05 PFLOP/s of visible pairs; one
-// chunk of 512 47 us in items of one query tile (51 us in two key ranges,
-// 72 us neither), one of 32 tokens 16 us (25 us with an empty second tile).
+// windows): 16 chunks of 512 tokens 530 to 600 us with the clock that the power
+// limit leaves, 0.90 to 1.02 PFLOP/s of visible pairs; one chunk of 512 47 us in
+// items of one query tile (51 us in two key ranges, 72 us neither), one of 32
+// tokens 16 us (25 us with an empty second tile).
 //
 // Warp 11 only completes the third warpgroup (setmaxnreg works per
 // warpgroup).  Every wait is bounded; a wait that gives up raises the CTA's abort flag, the

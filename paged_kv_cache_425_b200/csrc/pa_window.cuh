@@ -169,7 +169,7 @@ __device__ __forceinline__ uint2 narrow4(const float4 &v, float inv, __nv_bfloat
 // a run (tokens x group) <= 8 * NT.
 //
 // A warp takes every NW-th block of its CTA's blocks, U per step, and has
-// STAGES in flight.  Three shapes:
+// STAGES in flight.  Five shapes:
 //  * many rows (U = 1): 4 warps with one block each (two at head_dim 64), six
 //    CTAs per SM, partitions of PB blocks: the shape that reaches the memory's
 //    bandwidth best once the GPU is full.
@@ -177,11 +177,14 @@ __device__ __forceinline__ uint2 narrow4(const float4 &v, float inv, __nv_bfloat
 //    blocks, two CTAs per SM, for runs that fit in one such wave.  At one block
 //    per step a warp needs about 1300 cycles for the chain from scores to
 //    weights, which only many warps hide; two blocks are two chains.
+//  * at most a run per SM (U = 2, PB = 0, no cluster): the same with 6 or 8 warps,
+//    one CTA per SM (144 runs of 33 blocks 7.5 us, 10.3 with four warps; of 180
+//    blocks 36.0, 39.5 in partitions).
 //  * few rows (CLUSTER): the gridDim.y CTAs of a run, 6 or 8 warps each, form one
 //    thread-block cluster, take an equal share of its blocks each and send
 //    their results to each other's shared memory: one launch, no workspace.
 // Measured (bf16, 32 heads on 8, head_dim 128): 128 sequences with 4096-token
-// windows 312 us, 2.16 GB of visible rows at 6.9 TB/s (a copy reaches 6.55; L2
+// windows 311 us, 2.16 GB of visible rows at 6.9 TB/s (a copy reaches 6.55; L2
 // keeps a part between calls); 32 with 512-token windows, one wave, 10.9 us (15.8
 // in partitions); one with an 8192-token window in clusters of ten 10.4 us (13.5
 // in partitions).

@@ -160,9 +160,12 @@ inline WindowPlan window_plan(const WindowDevice &dev, int64_t num_seqs, int32_t
         p.warp_runs = true;
         return p;
     }
-    // 512-token partitions, or 1024 where that still makes several of a run
-    // (1024 runs of 258 blocks: 314 us, 325 with the shorter ones; 384 runs of
-    // up to 131: 63.3 and 61.7)
+    // 512-token partitions, or 1024 where that still makes several of a run:
+    // 320, 512 and 1024 runs of equal length, and of lengths up to twice the
+    // window.  Of 258 to 560 blocks the longer ones take 0.97 to 1.01 of the
+    // shorter ones' time (320 ragged runs of 258: 1.08); of 132 to 250 blocks 0.98
+    // to 1.09 (512 runs of 132: 89.5 us, 95.3 with the longer ones; 320 ragged
+    // runs of 132: 46.2 and 42.7).
     p.part_blocks = blocks >= 8 * kPartBlocks ? 2 * kPartBlocks : kPartBlocks;
     p.parts = (blocks + p.part_blocks - 1) / p.part_blocks;
     return p;
